@@ -351,6 +351,102 @@ BSA_API bsa_status bsa_attention_noalloc(const bsa_layout* layout, const void* q
                                          void* out, int32_t* status_dev, bsa_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * Paged key/value cache: streams of frames. The pages compute the global attention over all
+ * frames at once and have no counterpart; these calls serve frames that arrive one after the
+ * other: the keys and values of earlier tokens stay in a cache, the new tokens of a frame (or
+ * any chunk of new tokens, down to one) are appended to it and attend over it.
+ *
+ * A cache holds `seqs` independent sequences (streams) of tokens at positions 0, 1, ... in
+ * pages of `page_tokens` tokens. Pools are head-major inside a page:
+ *   k, v             : device, [pages, kv_heads, page_tokens, 64], bf16 or e4m3
+ *   k_scale, v_scale : e4m3: device, one byte per row [pages, kv_heads, page_tokens], the
+ *                      biased exponent e + 127 of the row's scale 2^e (255: the row is NaN);
+ *                      bf16: unused (NULL)
+ *   page_table       : device, int32 [seqs, max_pages]; entry t is the page of positions
+ *                      [t page_tokens, (t + 1) page_tokens), or negative: no page (never
+ *                      given, or taken back: its tokens no longer exist for the attention)
+ *   kv_len           : device, int32 [seqs], tokens of each sequence, the new ones included
+ * Grouped heads: query head h reads key/value head h / (heads / kv_heads).
+ * Packed rows: the new tokens of all sequences lie one after the other; those of sequence s
+ * are rows cu_new[s] .. cu_new[s + 1] - 1 (device, int32 [seqs + 1], ascending from 0), at
+ * positions kv_len[s] - n_s, ..., kv_len[s] - 1 with n_s = cu_new[s + 1] - cu_new[s] (0
+ * allowed). Rows at or past cu_new[seqs] are neither read nor written. `rows` is the number of
+ * rows the tensors have; row strides are in elements (a multiple of 8).
+ * All tables are read on the device when the call runs: a captured call replays with whatever
+ * the tables then hold. Table entries out of range (a page >= pages, a position past max_pages,
+ * n_s > kv_len[s], cu_new not ascending or past `rows`) are reported as BSA_ERR_DEVICE_BOUNDS
+ * through status_dev and their accesses skipped. Rows of a page that several sequences share
+ * may be read by all of them; two rows appended to one place in one call are a race.
+ * Limits (BSA_ERR_UNSUPPORTED): head_dim 64; page_tokens 16, 32, 64, 128 or 256; seqs <=
+ * BSA_KV_MAX_SEQS; heads <= BSA_MAX_HEADS; pages * kv_heads * page_tokens, max_pages *
+ * page_tokens, rows * heads < 2^31.
+ */
+#define BSA_KV_MAX_SEQS 1024
+typedef enum { BSA_KV_BF16 = 0, BSA_KV_E4M3 = 1 } bsa_kv_format;
+typedef struct {
+    int32_t seqs;        /* >= 1 */
+    int32_t heads;       /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;    /* >= 1 */
+    int32_t head_dim;    /* only 64 */
+    int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+    int32_t pages;       /* pages in the pools, >= 1 */
+    int32_t max_pages;   /* entries of a page-table row, >= 1 */
+    bsa_kv_format format;
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+} bsa_kv_cache;
+
+/* Appends the new tokens' keys and values. bf16: bits copied. e4m3: per row x of 64 values,
+ * a = max |x_i|, e = the smallest exponent with a <= 448 2^e, kept within [BSA_KV_EXP_MIN,
+ * BSA_KV_EXP_MAX] (a = 0: BSA_KV_EXP_MIN); x_i 2^-e is rounded to e4m3 (nearest, ties to even;
+ * magnitudes above 448 become 448). A power of two as scale makes code * 2^e exact in bf16. A
+ * row that holds an infinite or NaN element becomes all NaN (scale byte 255). Infinite and NaN
+ * elements, and for e4m3 magnitudes above 448 2^BSA_KV_EXP_MAX (14,680,064), are reported as
+ * BSA_ERR_RANGE.
+ *   k, v : device, bf16 [rows, kv_heads, 64] with row_stride elements between rows
+ * A new token without a page is reported as BSA_ERR_DEVICE_BOUNDS and dropped. */
+#define BSA_KV_EXP_MIN (-64)
+#define BSA_KV_EXP_MAX 15
+BSA_API bsa_status bsa_kv_append(const bsa_kv_cache* cache, int32_t rows, const int32_t* cu_new, const void* k,
+                                 const void* v, int64_t row_stride, int32_t* status_dev, bsa_stream_t stream);
+
+/* Reads cached tokens back as bf16 (e4m3: code * 2^e, exact): row i of sequence s (rows
+ * cu_rows[s] .. cu_rows[s + 1] - 1) is position first[s] + i. Positions without a page read as
+ * zeros; positions below 0 or at or past kv_len[s] read as zeros and are reported.
+ *   cu_rows : device, int32 [seqs + 1];  first : device, int32 [seqs]
+ *   k, v    : device, bf16 [rows, kv_heads, 64] with row_stride elements between rows */
+BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const int32_t* cu_rows, const int32_t* first,
+                               void* k, void* v, int64_t row_stride, int32_t* status_dev, bsa_stream_t stream);
+
+/* Attention of the new tokens over the cache, which holds them already (bsa_kv_append first).
+ * The token at position p of a sequence sees position j < kv_len if j's page exists and
+ *   unit > 0   : j < (floor(p / unit) + 1) unit -- causal over units of `unit` tokens: 1 =
+ *                token by token, tokens per frame = frame by frame; 0: every position
+ *   window > 0 : (unit > 0 only) and j >= (floor(p / unit) - window + 1) unit, or j < sink:
+ *                the last `window` units and the first `sink` tokens of the sequence
+ * out = softmax over the seen positions of (q . k / sqrt(64)), times V; lse = ln sum exp of the
+ * same scores. A token that sees nothing gets out = 0 and lse = -inf. Keys and values at
+ * positions that a token does not see never reach its result, whatever they hold; a NaN or
+ * infinite value that it does see makes the elements it enters non-finite.
+ *   max_new   : the largest n_s, or an upper bound; only the choice of kernel depends on it
+ *   q, out    : device, bf16 [rows, heads, 64] with q_stride, out_stride elements between rows
+ *   lse       : device, float32 [heads, rows], or NULL
+ *   workspace : device, 16-byte aligned, bsa_kv_workspace_size() bytes; needs no clearing and
+ *               keeps nothing between calls; calls that may overlap need one each
+ * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product. */
+BSA_API bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max_new, int32_t unit,
+                                    int32_t window, int32_t sink, const int32_t* cu_new, const void* q,
+                                    int64_t q_stride, void* out, int64_t out_stride, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* status_dev, bsa_stream_t stream);
+/* Bytes of bsa_kv_attention's workspace on the current device: the partial results of rows
+ * whose keys are split over several blocks. */
+BSA_API bsa_status bsa_kv_workspace_size(const bsa_kv_cache* cache, size_t* bytes);
+
+/* ---------------------------------------------------------------------------------
  * Self-check of the bounded device waits (no counterpart on the pages). Launches one
  * thread that waits, with the same bounded wait as the attention kernels, on an
  * mbarrier that nothing arrives on. After limit_us microseconds the wait gives up and

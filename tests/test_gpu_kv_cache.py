@@ -1,0 +1,457 @@
+"""The paged key/value cache on a B200 against the fp64 oracle (oracle/kv_cache.py): appending and reading
+back bit for bit, the attention within the bound of its roundings (tests/kv_common.py), the masks that leave
+rows empty, stale and non-finite memory, bad tables, strides, streams, captured calls, and a stream of frames
+through AttentionBlock."""
+import numpy as np
+import pytest
+
+from kv_common import D, Case, attention_oracle, bf16, cache_over, check_attention, tensors
+from oracle import kv_cache as okv
+from oracle import layer_io
+from view_transformers_b200 import _lib
+
+pytestmark = pytest.mark.gpu
+
+
+def _attend(c, x, cache=None, **kw):
+    import torch
+    cache = cache or cache_over(c, x)
+    out = torch.full((x["rows"], c.heads, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.heads, x["rows"]), 7.0, dtype=torch.float32, device="cuda")
+    cache.attend(x["q"], x["cu"], kw.pop("max_new", x["max_new"]), unit=c.unit, window=c.window, sink=c.sink, out=out,
+                 lse=lse, **kw)
+    return cache, out, lse
+
+
+ATTEND = [
+    # single tokens
+    Case("one_key", (1,), (1,)),
+    Case("one_15", (1,), (15,), heads=1, kv_heads=1),
+    Case("one_16", (1,), (16,), page=32),
+    Case("one_129_e4m3", (1,), (129,), page=64, fmt="e4m3"),
+    Case("one_long", (1,), (5001,), heads=3, kv_heads=3, page=64, scale=3.0),
+    Case("one_long_e4m3", (1,), (4999,), heads=2, kv_heads=1, page=128, fmt="e4m3", scale=3.0),
+    Case("one_256_page", (1,), (700,), page=256, unit=1),
+    # grouped heads: 4, 8 (one 8-row tile), 12 and 16 rows
+    Case("group4", (1, 1), (300, 33), heads=8, kv_heads=2, unit=1),
+    Case("group8_e4m3", (1,), (257,), heads=8, kv_heads=1, fmt="e4m3", page=32),
+    Case("rows12", (3,), (200,), heads=8, kv_heads=2, unit=1, page=32),
+    Case("rows15_e4m3", (5,), (333,), heads=6, kv_heads=2, unit=1, page=64, fmt="e4m3"),
+    # chunks
+    Case("chunk17", (17,), (17,), unit=1),
+    Case("chunk33_e4m3", (33,), (400,), unit=1, page=64, fmt="e4m3", scale=2.0),
+    Case("chunk128", (128,), (128,), unit=0, page=128),
+    Case("chunk129", (129,), (515,), heads=4, kv_heads=2, unit=1, page=64),
+    Case("chunk130_e4m3", (130,), (1000,), heads=1, kv_heads=1, unit=69, page=32, fmt="e4m3"),
+    Case("frame_782", (300,), (1111,), heads=1, kv_heads=1, unit=150, page=64),
+    Case("group3_chunk", (100,), (260,), heads=6, kv_heads=2, unit=1, page=16),
+    Case("group8_chunk_e4m3", (37,), (600,), heads=8, kv_heads=1, unit=1, page=16, fmt="e4m3"),
+    # windows and sinks
+    Case("window", (70,), (900,), unit=50, window=3, page=16),
+    Case("window_sink", (70,), (900,), unit=50, window=2, sink=21, page=64),
+    Case("window_sink_e4m3", (5,), (900,), unit=7, window=2, sink=130, page=16, fmt="e4m3"),
+    Case("window_one_token", (40,), (500,), unit=1, window=1, page=32),
+    Case("window_tiles", (200,), (1500,), heads=1, kv_heads=1, unit=1, window=300, sink=140, page=64),
+    Case("window_beyond", (9,), (100,), unit=10, window=50, sink=1000),
+    # several sequences, some without new tokens, some without anything
+    Case("ragged", (3, 0, 40, 1), (50, 20, 300, 1), heads=4, kv_heads=2, unit=1),
+    Case("empty_seq", (0, 2, 0), (0, 2, 0), unit=1),
+    Case("many", tuple([1] * 70), tuple(range(1, 211, 3)), heads=2, kv_heads=1, fmt="e4m3"),
+    Case("many_mixed", tuple([i % 5 for i in range(33)]), tuple([7 * i % 200 + 5 for i in range(33)]), unit=1),
+    Case("long_and_short", (140, 1, 1), (900, 2000, 3), heads=2, kv_heads=2, unit=1, page=64),
+    # evicted pages; the last case leaves every row empty
+    Case("evicted", (20,), (400,), unit=1, evict=((0, 0), (0, 3), (0, 4), (0, 9))),
+    Case("evicted_e4m3", (1, 2), (400, 90), page=32, fmt="e4m3", evict=((0, 0), (1, 1))),
+    Case("evicted_chunk", (200,), (600,), unit=1, page=64, evict=((0, 1), (0, 7))),
+    Case("all_evicted", (2,), (40,), evict=((0, 0), (0, 1), (0, 2))),
+    Case("all_evicted_chunk", (150,), (300,), page=64, evict=tuple((0, i) for i in range(5))),
+    Case("window_evicted", (150,), (600,), unit=10, window=2, page=16, evict=tuple((0, i) for i in range(29, 34))),
+]
+
+
+@pytest.mark.parametrize("c", ATTEND, ids=str)
+def test_attention_against_the_oracle(c):
+    import torch
+    x, host = tensors(c)
+    cache, out, lse = _attend(c, x)
+    assert cache.check_status() == 0
+    want = attention_oracle(c, host)
+    check_attention(out, lse, want)
+    # the same bits again, and whatever kernel max_new picks (each within the bound)
+    _, out2, lse2 = _attend(c, x, cache)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    for mx in (1, 2000):
+        _, out3, lse3 = _attend(c, x, cache, max_new=mx)
+        check_attention(out3, lse3, want)
+    assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 24, 200])
+def test_many_ranges_of_lengths(n, fmt):
+    """Lengths around the borders of steps (16), units (128) and pages."""
+    for m in (1, 2, 15, 16, 17, 31, 127, 128, 129, 255, 256, 257, 383, 385, 640):
+        if m < n:
+            continue
+        c = Case(f"len{m}", (n,), (m,), heads=1, kv_heads=1, page=32, fmt=fmt, unit=1)
+        x, host = tensors(c, seed=m)
+        cache, out, lse = _attend(c, x)
+        check_attention(out, lse, attention_oracle(c, host))
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 150])
+def test_nan_of_a_later_token_stays_with_those_that_see_it(fmt, n):
+    import torch
+    c = Case("nan", (n,), (n + 50,), heads=1, kv_heads=1, page=16, fmt=fmt, unit=1)
+    x, host = tensors(c)
+    pos = n + 50 - 2                                         # the last token but one
+    page, slot = int(x["table"][0, pos // 16]), pos % 16
+    if fmt == "bf16":
+        x["v_pool"][page, 0, slot, 5] = float("nan")
+        x["v_pool"][page, 0, slot, 40] = float("inf")
+    else:
+        x["v_scale"].view(torch.uint8)[page, 0, slot] = 255  # the row stands for NaN
+    cache, out, lse = _attend(c, x)
+    o, l, bo, bl = attention_oracle(c, host)
+    k = n - 2                                                # rows before do not see it
+    check_attention(out[:k], lse[:, :k], (o[:k], l[:, :k], bo[:k], bl[:, :k]))
+    bad = ~torch.isfinite(out[k:, 0].float())
+    assert bool((bad[:, 5] & bad[:, 40]).all()) if fmt == "bf16" else bool(bad.all())
+    if fmt == "bf16":
+        assert not bool(bad[:, [0, 4, 6, 39, 41, 63]].any())
+    # and a key that is NaN spoils the rows that see it, no other
+    x, host = tensors(c)
+    if fmt == "bf16":
+        x["k_pool"][page, 0, slot, 5] = float("nan")
+    else:
+        x["k_scale"].view(torch.uint8)[page, 0, slot] = 255
+    _, out, lse = _attend(c, x)
+    check_attention(out[:k], lse[:, :k], (o[:k], l[:, :k], bo[:k], bl[:, :k]))
+    assert bool(torch.isnan(out[k:].float()).all())
+
+
+def _fresh(c, device="cuda"):
+    """A cache with its tables set, empty pools of a sentinel, and the new tokens."""
+    import torch
+    x, host = tensors(c)
+    for n in ("k_pool", "v_pool"):
+        x[n].view(torch.uint8).fill_(0x55)
+        if c.fmt == "e4m3":
+            x[n[0] + "_scale"].view(torch.uint8).fill_(0x55)
+    return x, host
+
+
+APPEND = [
+    Case("a_one", (1,), (1,), fmt="e4m3"), Case("a_one_bf16", (1,), (33,)),
+    Case("a_frame", (69,), (200,), heads=3, kv_heads=3, page=32, fmt="e4m3"),
+    Case("a_ragged", (5, 0, 37, 1), (5, 9, 64, 300), heads=4, kv_heads=2, page=64),
+    Case("a_ragged_e4m3", (5, 0, 37, 1), (5, 9, 64, 300), heads=4, kv_heads=2, page=64, fmt="e4m3"),
+    Case("a_many", tuple([i % 3 for i in range(200)]), tuple([20 + i % 7 for i in range(200)]), fmt="e4m3"),
+    Case("a_long", (3000,), (3001,), heads=4, kv_heads=4, page=128, fmt="e4m3"),
+]
+
+
+@pytest.mark.parametrize("strided", [False, True], ids=["packed", "strided"])
+@pytest.mark.parametrize("c", APPEND, ids=str)
+def test_append_and_read_back(c, strided):
+    import torch
+    x, _ = _fresh(c)
+    rng = np.random.default_rng(5)
+    rows, Hk, P = x["rows"], c.kv_heads, c.page
+    kv = rng.standard_normal((2, rows, Hk, D)) * 2.0 ** rng.integers(-70, 13, (2, rows, Hk, 1))
+    kv[:, ::7] = 0.0
+    kv[0, ::5, :, 3] = 448 * 2.0 ** rng.integers(-20, 5)                  # a largest element on the border
+    kv = bf16(kv)
+    dev = torch.from_numpy(kv).to(torch.bfloat16).cuda()
+    if strided:                                                           # rows inside a wider tensor
+        wide = torch.full((2, rows + 1, Hk + 3, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        wide[:, :rows, 1:Hk + 1] = dev
+        dev = wide[:, :rows, 1:Hk + 1]
+    cache = cache_over(c, x)
+    cache.append(dev[0], dev[1], x["cu"])
+    assert cache.check_status() == 0
+    table, cu = x["table"].cpu().numpy(), x["cu"].cpu().numpy()
+    for which, n in enumerate("kv"):
+        pool = x[n + "_pool"].float().cpu().double().numpy()
+        raw = x[n + "_pool"].view(torch.uint8).cpu().numpy()
+        touched = np.zeros(pool.shape[:3], dtype=bool)
+        for s, (m, k) in enumerate(zip(c.lens, c.new)):
+            for i in range(k):
+                pos = m - k + i
+                pg, slot = table[s, pos // P], pos % P
+                touched[pg, :, slot] = True
+                row = kv[which, cu[s] + i]
+                if c.fmt == "e4m3":
+                    vals, e = okv.quantise(row)
+                    assert np.array_equal(pool[pg, :, slot], vals)
+                    assert np.array_equal(x[n + "_scale"].view(torch.uint8)[pg, :, slot].cpu().numpy(), e + 127)
+                else:
+                    assert np.array_equal(pool[pg, :, slot], row)
+        assert (raw[~touched] == 0x55).all()                              # nothing else was written
+    # read back: exactly what the cache holds, into a strided destination too
+    first = torch.tensor([m - k for m, k in zip(c.lens, c.new)], dtype=torch.int32, device="cuda")
+    wide = torch.full((2, rows + 2, Hk + 1, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = (wide[0, :rows, :Hk], wide[1, :rows, :Hk]) if strided else None
+    got = cache.read(x["cu"], first, rows=rows, out=got)
+    assert cache.check_status() == 0
+    for which in range(2):
+        want = kv[which]
+        if c.fmt == "e4m3":
+            want = okv.dequantise(*okv.quantise(want))
+        assert np.array_equal(got[which].double().cpu().numpy(), want)
+    if strided:
+        assert bool((wide[:, rows:] == 3).all()) and bool((wide[:, :, Hk:] == 3).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_append_reports_what_the_format_cannot_hold(fmt):
+    import torch
+    c = Case("r", (4,), (4,), heads=1, kv_heads=1, fmt=fmt)
+    ok = torch.ones((4, 1, D), dtype=torch.bfloat16, device="cuda")
+    for where, value, code in ((0, float("nan"), 6), (1, float("-inf"), 6), (0, 1.5e7, 6 if fmt == "e4m3" else 0),
+                               (1, 14680064.0, 0), (0, 3e38, 6 if fmt == "e4m3" else 0)):
+        x, _ = _fresh(c)
+        cache = cache_over(c, x)
+        kv = [ok.clone(), ok.clone()]
+        kv[where][2, 0, 17] = value
+        cache.append(kv[0], kv[1], x["cu"])
+        assert cache.check_status() == code, (value, fmt)
+        got = cache.read(x["cu"], torch.zeros(1, dtype=torch.int32, device="cuda"), rows=4)[where].float()
+        if not np.isfinite(value):
+            if fmt == "e4m3":
+                assert bool(torch.isnan(got[2]).all())                   # the whole row
+            else:
+                assert torch.equal(got[2, 0, 17].isnan(), torch.tensor(value).isnan().cuda())
+        elif fmt == "e4m3" and code:
+            assert float(got[2, 0, 17]) == 14680064.0                    # saturated
+        keep = [0, 1, 3]
+        assert bool((got[keep] == 1).all())
+
+
+def test_read_of_missing_tokens():
+    import torch
+    c = Case("m", (1, 1), (50, 20), page=16, evict=((0, 1),))
+    x, host = tensors(c)
+    cache = cache_over(c, x)
+    cu = torch.tensor([0, 40, 60], dtype=torch.int32, device="cuda")
+    k, v = cache.read(cu, torch.tensor([10, 0], dtype=torch.int32, device="cuda"), rows=60)
+    assert cache.check_status() == 0                                     # a missing page is no error
+    want = np.concatenate([np.where(host["gone"][0][10:50, None, None], 0, host["k"][0][10:50]), host["k"][1]])
+    assert np.array_equal(k.double().cpu().numpy(), want)
+    # past the end, before the start: zeros, reported
+    for first in ([11, 0], [-1, 0]):
+        k, v = cache.read(cu, torch.tensor(first, dtype=torch.int32, device="cuda"), rows=60)
+        assert cache.check_status() == _lib.BSA_ERR_DEVICE_BOUNDS
+        assert bool((v[39 if first[0] > 0 else 0] == 0).all())
+
+
+@pytest.mark.parametrize("n", [2, 40, 200])
+def test_rows_behind_the_last_sequence_stay(n):
+    import torch
+    c = Case("behind", (n,), (n + 60,), unit=1)
+    x, host = tensors(c)
+    q = torch.cat([x["q"], torch.full((9, c.heads, D), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    x2 = {**x, "q": q, "rows": n + 9}
+    cache, out, lse = _attend(c, x2)
+    assert cache.check_status() == 0
+    assert bool((out[n:] == 7).all()) and bool((lse[:, n:] == 7).all())
+    check_attention(out[:n], lse[:, :n].contiguous(), attention_oracle(c, host))
+    # appending and reading with more rows than the offsets name
+    before = x["k_pool"].view(torch.int16).clone()
+    kv = torch.full((n + 9, c.kv_heads, D), 2.0, dtype=torch.bfloat16, device="cuda")
+    cache.append(kv, kv, x["cu"])
+    assert int((x["k_pool"].view(torch.int16) != before).sum()) <= n * c.kv_heads * D
+    k = torch.full_like(kv, 5.0)
+    cache.read(x["cu"], x["kv_len"] - n, out=(k, k.clone()))
+    assert bool((k[n:] == 5).all()) and bool((k[:n] == 2).all()) and cache.check_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_bad_tables_are_reported_and_skipped(n, fmt):
+    """Every entry is bounds-checked on the device before it is used."""
+    import torch
+    c = Case("bad", (n, n), (n + 100, n + 30), page=16, unit=1, fmt=fmt)
+    kv = torch.zeros((2 * n, 2, D), dtype=torch.bfloat16, device="cuda")
+    two = lambda a, b: torch.tensor([a, b], dtype=torch.int32, device="cuda")
+    for what in ("page", "len", "neg_len", "cu", "cu_neg", "short"):
+        x, host = tensors(c)
+        if what == "page":
+            x["table"][0, 2] = x["k_pool"].shape[0]
+        elif what == "len":
+            x["kv_len"][0] = 1 << 30
+        elif what == "neg_len":
+            x["kv_len"][0] = -5
+        elif what == "cu":
+            x["cu"][1] = 5 * n
+        elif what == "cu_neg":
+            x["cu"][0] = -3
+        else:
+            x["kv_len"][0] = n - 1                         # fewer cached than new
+        cache, out, lse = _attend(c, x)
+        assert cache.check_status() == _lib.BSA_ERR_DEVICE_BOUNDS, what
+        if what in ("page", "len", "neg_len", "short"):    # the other sequence is not touched by it
+            o, l, bo, bl = attention_oracle(c, host)
+            check_attention(out[n:], lse[:, n:].contiguous(), (o[n:], l[:, n:], bo[n:], bl[:, n:]))
+        cache.append(kv, kv, x["cu"])
+        if what == "page":                                 # no new token lies on that page
+            cache.check_status()
+        else:
+            assert cache.check_status() == _lib.BSA_ERR_DEVICE_BOUNDS, what
+        cache.read(x["cu"], two(0, 0), rows=2 * n)
+        cache.check_status()
+    x, _ = tensors(c)
+    x["table"][1] = -1                                     # a new token without a page
+    cache = cache_over(c, x)
+    cache.append(kv, kv, x["cu"])
+    assert cache.check_status() == _lib.BSA_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 140])
+def test_strided_queries_and_outputs_on_another_stream(n, fmt):
+    import torch
+    c = Case("strided", (n,), (n + 333,), heads=4, kv_heads=2, page=32, unit=1, fmt=fmt)
+    x, host = tensors(c)
+    side = torch.cuda.Stream()
+    wide = torch.full((n, 7, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:5] = x["q"]
+    out = torch.full((n, 6, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((4, n), dtype=torch.float32, device="cuda")
+    cache = cache_over(c, x)
+    side.wait_stream(torch.cuda.current_stream())
+    cache.attend(wide[:, 1:5], x["cu"], n, unit=1, out=out[:, 1:5], lse=lse, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    check_attention(out[:, 1:5], lse, attention_oracle(c, host))
+    assert bool((out[:, [0, 5]] == 5).all())
+    got = cache.attend(x["q"], x["cu"], n, unit=1)                        # own output, no lse
+    assert torch.equal(got, out[:, 1:5]) and cache.check_status(side.cuda_stream) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_captured_calls_follow_the_tables(fmt):
+    """A captured append + attend replays for the next tokens after the tables moved on; two graphs that share
+    the cache's workspace replay one after the other."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    H, P = 2, 16
+    cache = KVCache(1, H, H, pages=16, page_tokens=P, max_pages=16, fmt=fmt)
+    rng = np.random.default_rng(3)
+    total, chunk = 180, 6
+    host = {n: bf16(rng.standard_normal((total, H, D))) for n in "qkv"}
+    dev = {n: torch.from_numpy(host[n]).to(torch.bfloat16).cuda() for n in "qkv"}
+    buf = {n: torch.zeros((chunk, H, D), dtype=torch.bfloat16, device="cuda") for n in "qkv"}
+    out, one = (torch.zeros((chunk, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.zeros((H, chunk), dtype=torch.float32, device="cuda")
+    cu = torch.tensor([0, chunk], dtype=torch.int32, device="cuda")
+    cache.append(buf["k"], buf["v"], cu)                                  # warm-up: kv_len 0, reported and dropped
+    cache.attend(buf["q"], cu, chunk, unit=1, out=out, lse=lse)
+    assert cache.check_status() == _lib.BSA_ERR_DEVICE_BOUNDS
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        cache.append(buf["k"], buf["v"], cu)
+        cache.attend(buf["q"], cu, chunk, unit=1, out=out, lse=lse)
+    with torch.cuda.graph(g2):
+        cache.attend(buf["q"], cu, 200, unit=1, out=one)                  # the form for many rows
+    for at in range(0, total, chunk):
+        cache.extend([chunk])
+        for n in "qkv":
+            buf[n].copy_(dev[n][at:at + chunk])
+        g1.replay()
+        g2.replay()
+        if at in (0, 6, 60, 126, 132, 174):
+            m = at + chunk
+            c = Case("g", (chunk,), (m,), heads=H, kv_heads=H, unit=1, fmt=fmt)
+            k, v = (okv.dequantise(*okv.quantise(host[n][:m])) if fmt == "e4m3" else host[n][:m] for n in "kv")
+            want = attention_oracle(c, {"q": [host["q"][at:m]], "k": [k], "v": [v], "gone": [np.zeros(m, bool)]})
+            check_attention(out, lse, want)
+            check_attention(one, lse, want)
+    assert cache.check_status() == 0
+    K, V = cache.read_all(0)
+    assert np.array_equal(K.double().cpu().numpy(), okv.dequantise(*okv.quantise(host["k"])) if fmt == "e4m3" else host["k"])
+
+
+def test_two_caches_over_one_pool_on_two_streams():
+    import torch
+    cs = [Case("a", (1,), (3000,), page=64), Case("a", (1,), (3000,), page=64, unit=1)]
+    x, host = tensors(cs[0])
+    caches = [cache_over(c, x) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for c, cache, st in zip(cs, caches, streams):
+            with torch.cuda.stream(st):
+                outs.append(cache.attend(x["q"], x["cu"], 1, unit=c.unit))
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("n,fmt", [(1, "bf16"), (9, "e4m3"), (150, "bf16"), (150, "e4m3")])
+def test_no_writes_outside_the_buffers(n, fmt):
+    import torch
+    from test_gpu_canary import Guarded
+    c = Case("canary", (n, 3), (n + 200, 40), heads=4, kv_heads=2, page=16, unit=1, fmt=fmt)
+    x, host = tensors(c)
+    cache = cache_over(c, x)
+    rows = x["rows"]
+    g = {"out": Guarded(torch, rows * 4 * D * 2), "lse": Guarded(torch, rows * 4 * 4),
+         "ws": Guarded(torch, cache.ws_bytes), "k": Guarded(torch, rows * 2 * D * 2), "v": Guarded(torch, rows * 2 * D * 2)}
+    st = torch.cuda.current_stream().cuda_stream
+    first = torch.zeros(2, dtype=torch.int32, device="cuda")
+    sp = cache.status.data_ptr()
+    _lib.bsa_kv_attention(cache.c, rows, n, 1, 0, 0, x["cu"].data_ptr(), x["q"].data_ptr(), 4 * D, g["out"].ptr, 4 * D,
+                          g["lse"].ptr, g["ws"].ptr, cache.ws_bytes, sp, st)
+    _lib.bsa_kv_read(cache.c, rows, x["cu"].data_ptr(), first.data_ptr(), g["k"].ptr, g["v"].ptr, 2 * D, sp, st)
+    torch.cuda.synchronize()
+    assert not [k for k, b in g.items() if not b.intact()] and cache.check_status() == 0
+    got = g["out"].raw[g["out"].off:g["out"].off + rows * 4 * D * 2].view(torch.bfloat16).view(rows, 4, D)
+    lse = g["lse"].raw[g["lse"].off:g["lse"].off + rows * 16].view(torch.float32).view(4, rows)
+    check_attention(got, lse, attention_oracle(c, host))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_stream_of_frames_through_the_attention_block(fmt):
+    """Frames arrive one by one: projection, append, attention over the first frame and the last two,
+    output projection, each step against the oracle on the device's own tensors; then the cached scene is read
+    back and taken by the block-sparse layer."""
+    import torch
+    from oracle.compare import rel_l2
+    import oracle
+    from view_transformers_b200 import configs, layer, synth
+    from view_transformers_b200.cache import KVCache
+    T, H, frames = 133, 2, 5
+    w = configs.VGGT518.with_(name="kv_stream", frames=frames, heads=H, patch_per_frame=T - 5, tau=0.0)
+    bi = synth.make_block_inputs(w)
+    dev = lambda a: torch.from_numpy(a).cuda() if a.dtype == np.float32 else layer.to_device(a, "bf16")
+    x, wq, bq, wo, bo = (dev(a) for a in (bi.x, bi.w_qkv, bi.b_qkv, bi.w_o, bi.b_o))
+    cache = KVCache(1, H, H, pages=48, page_tokens=16, max_pages=48, fmt=fmt)
+    blk = layer.AttentionBlock(1, T, 5, H, D, wq, bq, wo, bo, cache=cache, window=2, anchor=1)
+    K, V = [], []
+    for f in range(frames):
+        y = blk.forward(x[f * T:(f + 1) * T].contiguous())
+        assert blk.check_status() == 0
+        q, k, v, o = (t.double().cpu().numpy() for t in (blk.q, blk.k, blk.v, blk.o))
+        for acc, t in ((K, k), (V, v)):
+            acc.append(okv.dequantise(*okv.quantise(t)) if fmt == "e4m3" else t)
+        m = (f + 1) * T
+        c = Case("s", (T,), (m,), heads=H, kv_heads=H, unit=T, window=2, sink=T, fmt=fmt)
+        ro, _, bnd, _ = attention_oracle(c, {"q": [q], "k": [np.concatenate(K)], "v": [np.concatenate(V)],
+                                             "gone": [np.zeros(m, bool)]})
+        assert np.max(np.abs(o - ro) / bnd) <= 1.0
+        ref = layer_io.out_project(o, synth.bf16_bits_to_f32(bi.w_o).astype(np.float64), bi.b_o)
+        assert rel_l2(y.double().cpu().numpy(), ref) <= 2e-3
+    assert cache.lengths == [frames * T]
+    k, v = cache.read_all(0)
+    assert np.array_equal(k.double().cpu().numpy(), np.concatenate(K))
+    assert np.array_equal(v.double().cpu().numpy(), np.concatenate(V))
+    L = layer.BlockSparseLayer.for_workload(w)
+    q = torch.randn_like(k)
+    out = L.forward(q, k, v).double().cpu().numpy()
+    assert L.check_status() == 0
+    lay = oracle.Layout(frames, T, 5, H, D, w.block)
+    want = oracle.layer_forward(q.double().cpu().numpy(), np.concatenate(K), np.concatenate(V), lay, L.selected())
+    assert rel_l2(out, want) <= 2e-3

@@ -26,6 +26,18 @@ class bsa_layout(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+BSA_KV_BF16, BSA_KV_E4M3 = 0, 1
+KV_FORMATS = {"bf16": BSA_KV_BF16, "e4m3": BSA_KV_E4M3}
+
+
+class bsa_kv_cache(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("format", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
+
+
 class BsaError(RuntimeError):
     def __init__(self, fn: str, code: int, msg: str):
         super().__init__(f"{fn}: {msg} (status {code})")
@@ -34,7 +46,12 @@ class BsaError(RuntimeError):
 
 _vp, _sz, _i32p, _st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
 _LP = ctypes.POINTER(bsa_layout)
+_KP, _i32, _i64 = ctypes.POINTER(bsa_kv_cache), ctypes.c_int32, ctypes.c_int64
 _SIGS = {
+    "bsa_kv_append": [_KP, _i32, _vp, _vp, _vp, _i64, _i32p, _st],
+    "bsa_kv_read": [_KP, _i32, _vp, _vp, _vp, _vp, _i64, _i32p, _st],
+    "bsa_kv_attention": [_KP, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _i32p, _st],
+    "bsa_kv_workspace_size": [_KP, ctypes.POINTER(ctypes.c_size_t)],
     "bsa_pool_qk": [_LP, _vp, _vp, _vp, _vp, _i32p, _st],
     "bsa_predict_mask": [_LP, _vp, _vp, ctypes.c_double, ctypes.c_double, ctypes.c_void_p, _vp, _vp, _vp, _i32p, _st],
     "bsa_pack_qkv": [_LP, _vp, _vp, _vp, _vp, _sz, _i32p, _st],
@@ -270,3 +287,27 @@ def bsa_attention_noalloc(layout, q, k, v, kv_idx, kv_cnt, out, status=0, stream
     """Steps 4-6 for bf16 layers with the library's static scratch (no workspace argument)."""
     _check("bsa_attention_noalloc", load().bsa_attention_noalloc(
         ctypes.byref(layout), q, k, v, kv_idx, kv_cnt, out, status, stream))
+
+
+# ------------------------------------------------------------------ paged key/value cache
+
+def bsa_kv_workspace_size(cache) -> int:
+    out = ctypes.c_size_t()
+    _check("bsa_kv_workspace_size", load().bsa_kv_workspace_size(ctypes.byref(cache), ctypes.byref(out)))
+    return out.value
+
+
+def bsa_kv_append(cache, rows, cu_new, k, v, row_stride, status=0, stream=0) -> None:
+    _check("bsa_kv_append", load().bsa_kv_append(ctypes.byref(cache), rows, cu_new, k, v, row_stride, status, stream))
+
+
+def bsa_kv_read(cache, rows, cu_rows, first, k, v, row_stride, status=0, stream=0) -> None:
+    _check("bsa_kv_read", load().bsa_kv_read(ctypes.byref(cache), rows, cu_rows, first, k, v, row_stride, status,
+                                             stream))
+
+
+def bsa_kv_attention(cache, rows, max_new, unit, window, sink, cu_new, q, q_stride, out, out_stride, lse, workspace,
+                     workspace_bytes, status=0, stream=0) -> None:
+    _check("bsa_kv_attention", load().bsa_kv_attention(
+        ctypes.byref(cache), rows, max_new, unit, window, sink, cu_new, q, q_stride, out, out_stride, lse, workspace,
+        workspace_bytes, status, stream))

@@ -1,0 +1,270 @@
+"""Paged key/value cache for streams of frames, through the C ABI (bsa_kv_* in include/bsa.h).
+
+KVCache keeps the keys and values of the tokens seen so far; each new chunk of tokens (a frame,
+its camera and register tokens, one token) is appended and attends over the cache:
+
+    cache = KVCache(seqs=1, heads=16, kv_heads=16, pages=2048, page_tokens=64, max_pages=2048, fmt="e4m3")
+    chunk = cache.extend([782])                        # 782 new tokens of sequence 0: pages and lengths
+    cache.append(k, v, chunk.cu_new)                   # k, v: [782, 16, 64] bf16
+    o = cache.attend(q, chunk.cu_new, chunk.max_new, unit=782)     # frame-wise causal
+    K, V = cache.read_all(0)                           # [tokens, 16, 64] bf16, e.g. for a global layer
+
+A program that keeps its own pools and page tables wraps them with KVCache.over(...) and calls
+append / attend / read with its own offsets. Device tables are read when the kernels run, so
+captured calls replay with what the tables then hold.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+
+_POOL_DTYPE = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+
+
+@dataclass
+class Chunk:
+    """New tokens of every sequence: packed rows cu_new[s] .. cu_new[s + 1] - 1."""
+    cu_new: torch.Tensor
+    max_new: int
+    rows: int
+
+
+class KVCache:
+    """One layer's cache. Calls on one KVCache share its workspace and status word: calls that may
+    overlap on the GPU (other streams) need a KVCache each, over the same pools if need be."""
+
+    def __init__(self, seqs: int, heads: int, kv_heads: int, pages: int, page_tokens: int, max_pages: int,
+                 fmt: str = "bf16", head_dim: int = 64, device: str | torch.device = "cuda"):
+        if fmt not in _lib.KV_FORMATS:
+            raise ValueError(f"fmt must be one of {tuple(_lib.KV_FORMATS)}")
+        sizes = _lib.bsa_kv_cache(seqs, heads, kv_heads, head_dim, page_tokens, pages, max_pages,
+                                  _lib.KV_FORMATS[fmt])
+        _lib.bsa_kv_workspace_size(sizes)              # refuses what the kernels do not take
+        dev = _device(device)
+        shape = (pages, kv_heads, page_tokens, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8 if fmt == "e4m3" else torch.bfloat16, device=dev)
+                for _ in range(2))
+        ks = vs = None
+        if fmt == "e4m3":
+            k, v = k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+            ks, vs = (torch.zeros(shape[:3], dtype=torch.uint8, device=dev).view(torch.float8_e8m0fnu)
+                      for _ in range(2))
+        self._bind(k, v, ks, vs, torch.full((seqs, max_pages), -1, dtype=torch.int32, device=dev),
+                   torch.zeros(seqs, dtype=torch.int32, device=dev), heads)
+        self._table = torch.full((seqs, max_pages), -1, dtype=torch.int32)
+        self._free = list(range(pages - 1, -1, -1))
+        self.lengths = [0] * seqs
+
+    @classmethod
+    def over(cls, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, heads: int,
+             k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None) -> "KVCache":
+        """A cache over the caller's pools [pages, kv_heads, page_tokens, 64] (bf16, or e4m3 with scales
+        [pages, kv_heads, page_tokens]) and tables (page_table [seqs, max_pages], kv_len [seqs], int32). The
+        caller keeps the tables; extend, release, forget and read_all are not available."""
+        self = cls.__new__(cls)
+        self._bind(k, v, k_scale, v_scale, page_table, kv_len, heads)
+        self._table = None
+        return self
+
+    def _bind(self, k, v, k_scale, v_scale, page_table, kv_len, heads) -> None:
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _POOL_DTYPE.values():
+            raise ValueError("k and v must be bf16 or float8_e4m3fn pools [pages, kv_heads, page_tokens, head_dim]")
+        self.fmt = "bf16" if k.dtype == torch.bfloat16 else "e4m3"
+        pages, kv_heads, page_tokens, head_dim = k.shape
+        if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1]:
+            raise ValueError("page_table must be [seqs, max_pages] and kv_len [seqs]")
+        tensors = [k, v, page_table, kv_len]
+        if self.fmt == "e4m3":
+            for t in (k_scale, v_scale):
+                if t is None or t.shape != k.shape[:3] or t.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+                    raise ValueError("an e4m3 cache needs k_scale and v_scale, float8_e8m0fnu or uint8 "
+                                     "[pages, kv_heads, page_tokens]")
+                tensors.append(t)
+        if page_table.dtype != torch.int32 or kv_len.dtype != torch.int32:
+            raise ValueError("page_table and kv_len must be int32")
+        if any(t.device != k.device or not t.is_contiguous() for t in tensors):
+            raise ValueError("the cache's tensors must be contiguous and on one device")
+        self.device, self.heads, self.kv_heads, self.head_dim = k.device, heads, kv_heads, head_dim
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.kv_len, self.page_tokens = page_table, kv_len, page_tokens
+        ptr = (lambda t: None if t is None else t.data_ptr())
+        self.c = _lib.bsa_kv_cache(page_table.shape[0], heads, kv_heads, head_dim, page_tokens, pages,
+                                   page_table.shape[1], _lib.KV_FORMATS[self.fmt], ptr(k), ptr(v), ptr(k_scale),
+                                   ptr(v_scale), ptr(page_table), ptr(kv_len))
+        self.seqs = page_table.shape[0]
+        with self._on_device():
+            self.ws_bytes = _lib.bsa_kv_workspace_size(self.c)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._ref = ctypes.byref(self.c)
+        self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
+
+    # steps --------------------------------------------------------------------------
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, stream: int | None = None) -> None:
+        """Writes the new tokens' keys and values ([rows, kv_heads, 64] bf16, one row stride) to the ends
+        of their sequences, whose kv_len and pages count them already."""
+        rows, stride = self._rows("k", k, self.kv_heads)
+        if self._rows("v", v, self.kv_heads) != (rows, stride):
+            raise ValueError("k and v must have the same rows and row stride")
+        self._offsets("cu_new", cu_new, self.seqs + 1)
+        st, guard = self._stream(stream)
+        with guard:
+            _lib._check("bsa_kv_append", _lib.load().bsa_kv_append(
+                self._ref, rows, cu_new.data_ptr(), k.data_ptr(), v.data_ptr(), stride, self._status_ptr, st))
+
+    def attend(self, q: torch.Tensor, cu_new: torch.Tensor, max_new: int, unit: int = 0, window: int = 0,
+               sink: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               stream: int | None = None) -> torch.Tensor:
+        """Attention of the new tokens' queries ([rows, heads, 64] bf16) over their sequences, which hold
+        the tokens already. unit: tokens per causal unit (tokens per frame: frame-wise; 1: token-wise; 0: all
+        see all). window, sink: only the last `window` units and the first `sink` tokens. max_new: the most
+        new tokens of a sequence. lse: optional float32 [heads, rows] for ln sum exp."""
+        rows, stride = self._rows("q", q, self.heads)
+        if out is None:
+            out = torch.empty((rows, self.heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+            if stream is not None:
+                out.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+        out_rows, out_stride = self._rows("out", out, self.heads)
+        if out_rows != rows:
+            raise ValueError("out must have q's rows")
+        if lse is not None and (lse.shape != (self.heads, rows) or lse.dtype != torch.float32
+                                or lse.device != self.device or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor {(self.heads, rows)} on {self.device}")
+        self._offsets("cu_new", cu_new, self.seqs + 1)
+        st, guard = self._stream(stream)
+        with guard:
+            _lib._check("bsa_kv_attention", _lib.load().bsa_kv_attention(
+                self._ref, rows, max_new, unit, window, sink, cu_new.data_ptr(), q.data_ptr(), stride,
+                out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), self._ws_ptr, self.ws_bytes,
+                self._status_ptr, st))
+        return out
+
+    def read(self, cu_rows: torch.Tensor, first: torch.Tensor, rows: int | None = None, out=None,
+             stream: int | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """Positions first[s], first[s] + 1, ... of each sequence as packed bf16 rows (k, v)
+        [rows, kv_heads, 64]; tokens without a page read as zeros. `rows` or `out` = (k, v) sets the size."""
+        if out is None:
+            if rows is None:
+                raise ValueError("read needs rows or out")
+            shape = (rows, self.kv_heads, self.head_dim)
+            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
+            if stream is not None:
+                for x in out:
+                    x.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+        k, v = out
+        n, stride = self._rows("k", k, self.kv_heads)
+        if self._rows("v", v, self.kv_heads) != (n, stride):
+            raise ValueError("k and v must have the same rows and row stride")
+        self._offsets("cu_rows", cu_rows, self.seqs + 1)
+        self._offsets("first", first, self.seqs)
+        st, guard = self._stream(stream)
+        with guard:
+            _lib._check("bsa_kv_read", _lib.load().bsa_kv_read(
+                self._ref, n, cu_rows.data_ptr(), first.data_ptr(), k.data_ptr(), v.data_ptr(), stride,
+                self._status_ptr, st))
+        return k, v
+
+    def check_status(self, stream: int | None = None) -> int:
+        """Waits for the stream; the first device-side error since the last check (0: none)."""
+        st, guard = self._stream(stream)
+        with guard:
+            return _lib.bsa_check_status(self._status_ptr, st)
+
+    # pages and lengths kept by the cache itself ------------------------------------------
+    def extend(self, counts, stream: int | None = None) -> Chunk:
+        """Makes room for counts[s] new tokens of each sequence: takes pages, updates the device tables (in
+        stream order) and returns the chunk's offsets. Raises before any change if the pages do not suffice."""
+        self._own()
+        counts = [int(n) for n in counts]
+        if len(counts) != self.seqs or min(counts) < 0:
+            raise ValueError(f"extend needs {self.seqs} counts >= 0")
+        P, width = self.page_tokens, self._table.shape[1]
+        spans = [(-(-m // P), -(-(m + n) // P)) for m, n in zip(self.lengths, counts)]
+        if any(b > width for _, b in spans):
+            raise RuntimeError(f"a sequence would exceed max_pages = {width}")
+        if sum(b - a for a, b in spans) > len(self._free):
+            raise RuntimeError(f"{sum(b - a for a, b in spans)} pages needed, {len(self._free)} free")
+        cu = [0]
+        for s, (a, b) in enumerate(spans):
+            for t in range(a, b):
+                self._table[s, t] = self._free.pop()
+            self.lengths[s] += counts[s]
+            cu.append(cu[-1] + counts[s])
+        self._upload(stream)
+        with self._torch_stream(stream):
+            cu_new = torch.tensor(cu, dtype=torch.int32).to(self.device)
+        return Chunk(cu_new, max(counts), cu[-1])
+
+    def forget(self, seq: int, start: int, stop: int, stream: int | None = None) -> None:
+        """Gives back the pages that lie wholly inside positions [start, stop) of a sequence: their tokens no
+        longer exist for later calls. The sequence's last page, if not full, stays."""
+        self._own()
+        P = self.page_tokens
+        for t in range(-(-max(start, 0) // P), min(stop, self.lengths[seq]) // P):
+            if self._table[seq, t] >= 0:
+                self._free.append(int(self._table[seq, t]))
+                self._table[seq, t] = -1
+        self._upload(stream)
+
+    def release(self, seq: int, stream: int | None = None) -> None:
+        """Empties a sequence."""
+        self._own()
+        self._free += [int(p) for p in self._table[seq] if p >= 0]
+        self._table[seq] = -1
+        self.lengths[seq] = 0
+        self._upload(stream)
+
+    def read_all(self, seq: int, stream: int | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """Every position of a sequence, (k, v) [tokens, kv_heads, 64] bf16."""
+        self._own()
+        n = self.lengths[seq]
+        with self._torch_stream(stream):
+            cu = torch.tensor([0] * (seq + 1) + [n] * (self.seqs - seq), dtype=torch.int32).to(self.device)
+            first = torch.zeros(self.seqs, dtype=torch.int32, device=self.device)
+        return self.read(cu, first, rows=n, stream=stream)
+
+    # helpers ------------------------------------------------------------------------------
+    def _own(self) -> None:
+        if self._table is None:
+            raise RuntimeError("the caller keeps this cache's tables")
+
+    def _upload(self, stream) -> None:
+        with self._torch_stream(stream):
+            self.page_table.copy_(self._table)
+            self.kv_len.copy_(torch.tensor(self.lengths, dtype=torch.int32))
+
+    def _rows(self, name: str, x: torch.Tensor, heads: int) -> tuple[int, int]:
+        shape, stride = x.shape, x.stride()
+        if (len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim or x.dtype != torch.bfloat16
+                or x.device != self.device or stride[2] != 1 or stride[1] != self.head_dim):
+            raise ValueError(f"{name} must be a bf16 tensor [rows, {heads}, {self.head_dim}] on {self.device} whose "
+                             "rows are contiguous")
+        return shape[0], stride[0] if shape[0] > 1 else heads * self.head_dim
+
+    def _offsets(self, name: str, x: torch.Tensor, n: int) -> None:
+        if x.dtype != torch.int32 or x.shape != (n,) or x.device != self.device or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
+
+    def _on_device(self):
+        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device)
+
+    def _stream(self, stream):
+        st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        return st, self._on_device()
+
+    def _torch_stream(self, stream):
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device))
+
+
+def _device(device) -> torch.device:
+    dev = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev

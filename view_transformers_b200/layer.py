@@ -222,10 +222,24 @@ class AttentionBlock:
     """The projections around one attention layer of the aggregator: x [N, C] -> QKV projection
     -> attention (global block-sparse `layer`, or frame-wise when layer is None) -> output
     projection -> y [N, C] (bf16). Weights are device tensors: w_qkv [3C, C], b_qkv [3C] fp32 or
-    None, w_o [C, C], b_o [C] fp32 or None."""
+    None, w_o [C, C], b_o [C] fp32 or None.
+
+    With `cache` (a cache.KVCache of one sequence) the block serves a stream of frames: each call
+    takes the next `frames` frames, appends their keys and values to the cache and lets every
+    token attend over its own frame and the cached ones before it -- with window > 0 only the
+    last `window` frames (its own included) and the first `anchor` frames of the stream."""
 
     def __init__(self, frames: int, tokens_per_frame: int, special_per_frame: int, heads: int, head_dim: int,
-                 w_qkv, b_qkv, w_o, b_o, layer: "BlockSparseLayer | None" = None, device="cuda"):
+                 w_qkv, b_qkv, w_o, b_o, layer: "BlockSparseLayer | None" = None, device="cuda", cache=None,
+                 window: int = 0, anchor: int = 0):
+        if cache is not None:
+            if layer is not None:
+                raise ValueError("the attention is either a layer or over a cache")
+            if (cache.seqs, cache.heads, cache.kv_heads) != (1, heads, heads):
+                raise ValueError(f"the cache must hold one sequence of {heads} heads")
+        if (window or anchor) and cache is None:
+            raise ValueError("window and anchor need a cache")
+        self.cache, self.window, self.sink = cache, window, anchor * tokens_per_frame if window else 0
         self.layout = _lib.make_layout(frames, tokens_per_frame, special_per_frame, heads, head_dim,
                                        layer.layout.block if layer is not None else 128, "bf16")
         self.w_qkv, self.b_qkv, self.w_o, self.b_o = w_qkv, b_qkv, w_o, b_o
@@ -237,7 +251,7 @@ class AttentionBlock:
                                           for _ in range(4))
         self.y = torch.empty((N, heads * head_dim), dtype=torch.bfloat16, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self.frame_ws_bytes = _lib.bsa_frame_workspace_size(self.layout) if layer is None else 0
+        self.frame_ws_bytes = _lib.bsa_frame_workspace_size(self.layout) if layer is None and cache is None else 0
         self.frame_ws = torch.empty(self.frame_ws_bytes + 1024, dtype=torch.uint8, device=self.device)
         self.frame_ws_ptr = (self.frame_ws.data_ptr() + 1023) // 1024 * 1024
 
@@ -247,7 +261,12 @@ class AttentionBlock:
         ptr = (lambda t: 0 if t is None else t.data_ptr())
         _lib.bsa_qkv_project(self.layout, x.data_ptr(), self.w_qkv.data_ptr(), ptr(self.b_qkv), self.q.data_ptr(),
                              self.k.data_ptr(), self.v.data_ptr(), s, st)
-        if self.layer is None:
+        if self.cache is not None:
+            chunk = self.cache.extend([self.q.shape[0]], stream)
+            self.cache.append(self.k, self.v, chunk.cu_new, stream)
+            self.cache.attend(self.q, chunk.cu_new, chunk.max_new, unit=self.layout.tokens_per_frame,
+                              window=self.window, sink=self.sink, out=self.o, stream=stream)
+        elif self.layer is None:
             _lib.bsa_pack_frames(self.layout, self.q.data_ptr(), self.k.data_ptr(), self.v.data_ptr(),
                                  self.frame_ws_ptr, self.frame_ws_bytes, s, st)
             _lib.bsa_frame_attention(self.layout, self.frame_ws_ptr, self.frame_ws_bytes, self.o.data_ptr(), s, st)
@@ -262,6 +281,8 @@ class AttentionBlock:
         code = _lib.bsa_check_status(self.status.data_ptr(), st)
         if self.layer is not None:
             code = code or self.layer.check_status(stream)
+        if self.cache is not None:
+            code = code or self.cache.check_status(stream)
         return code
 
 
