@@ -9,6 +9,7 @@ cudaError_t launch_kv_copy(const kv::CacheArgs& c, bool fp8, bool read, int rows
                            const int32_t* first, const void* const src[2], void* const dst[2],
                            uint8_t* const scale[2], long long stride, int32_t* status, cudaStream_t st);
 cudaError_t launch_kv_rows(kv::AttnArgs& a, bool fp8, bool eight, cudaStream_t st);
+cudaError_t launch_kv_tc(kv::AttnArgs& a, bool fp8, cudaStream_t st);
 
 namespace {
 
@@ -58,7 +59,7 @@ bsa_status check_cache(const bsa_kv_cache* c, int32_t rows, kv::CacheArgs* a) {
 }
 
 bool bad_stride(int64_t stride, int64_t heads) {
-    return stride < heads * BSA_HEAD_DIM || stride % 8 != 0 || stride > (int64_t)1 << 40;
+    return stride < heads * BSA_HEAD_DIM || stride % 8 != 0 || stride > (int64_t)1 << 38;
 }
 
 // Blocks of the attention kernels: two per SM.
@@ -155,10 +156,10 @@ bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max
     a.status = status_dev;
     a.max_teams = max_blocks();
     a.R = 1;
-    a.min_run = 1;
     const bool fp8 = cache->format == BSA_KV_E4M3;
     const long long per_head = (long long)max_new * a.group;   // query rows of a key/value head, at most
-    return from_cuda(launch_kv_rows(a, fp8, per_head <= 8, reinterpret_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(per_head > 16 ? launch_kv_tc(a, fp8, st) : launch_kv_rows(a, fp8, per_head <= 8, st));
 }
 
 }  // extern "C"

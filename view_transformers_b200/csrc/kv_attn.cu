@@ -122,7 +122,7 @@ kv_rows_kernel(const AttnArgs a) {
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < M * 2) (&poison[0][0])[tid] = 0u;
-    plan<M>(a, team, reinterpret_cast<long long*>(smem),
+    plan(a, team, reinterpret_cast<long long*>(smem),
             reinterpret_cast<int*>(smem + sizeof(long long) * (BSA_KV_MAX_SEQS + 1)), &start);
     const Start st = start;
     if (tid == 0) a.desc[team * kDesc] = 0;
@@ -133,7 +133,7 @@ kv_rows_kernel(const AttnArgs a) {
     float* mml = mo + kWarps * M * 64;                                // [warp][row][2]
 
     // the loader runs kStages - 1 steps ahead of the arithmetic, across items
-    Walk<M> lw(a, st, team);
+    Walk lw(a, st, team);
     bool live = lw.next();
     int lj = live ? lw.j0 : 0;
     uint32_t held = 0u;                     // bit s: stage s holds keys
@@ -189,12 +189,12 @@ kv_rows_kernel(const AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load_step(i);
 
-    Walk<M> w(a, st, team);
+    Walk w(a, st, team);
     int stage = 0;
     while (w.next()) {
         const Seq q = w.q;
         const int nrows = q.n * a.group;
-        const int r0 = w.rg * M;            // R = 1: a row group is one query tile
+        const int r0 = w.rg * M;            // R = 1, mr = M: a row group is one query tile
         // ---------------------------------------------------------------- Q
         uint32_t qf[4][2 * NH];
         float rowf[NH];                     // x = score * rowf
@@ -525,8 +525,8 @@ kv_merge_kernel(const AttnArgs a) {
     const int* d = a.desc + team * kDesc;
     if (d[0] == 0) return;
     const int row0 = d[1], n = d[2], h = d[3], last = d[5];
-    const long long r0 = ((long long)d[4] * a.R + member) * M;
-    const int nrows = (int)min((long long)M, (long long)n * a.group - r0);
+    const long long r0 = ((long long)d[4] * a.R + member) * a.mr;
+    const int nrows = (int)min((long long)a.mr, (long long)n * a.group - r0);
     const int c4 = (threadIdx.x & 15) * 4;
     for (int r = threadIdx.x >> 4; r < nrows; r += 16) {
         float mx = part_at<M>(a, team, 1, member)[M * 64 + r];
@@ -567,7 +567,7 @@ cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
 }  // namespace
 
 template <int M>
-cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st) {
+static cudaError_t launch_merge(const AttnArgs& a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.max_teams * a.R);
     cfg.blockDim = dim3(256);
@@ -580,14 +580,19 @@ cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kv_merge_kernel<M>, a);
 }
 
+cudaError_t launch_kv_merge128(const AttnArgs& a, cudaStream_t st) { return launch_merge<128>(a, st); }
+
 cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
     cudaError_t e;
+    a.R = 1;
+    a.mr = eight ? 8 : 16;
+    a.min_run = 1;
     if (eight) {
         e = fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st);
-        return e != cudaSuccess ? e : launch_kv_merge<8>(a, st);
+        return e != cudaSuccess ? e : launch_merge<8>(a, st);
     }
     e = fp8 ? launch_rows<true, 16>(a, st) : launch_rows<false, 16>(a, st);
-    return e != cudaSuccess ? e : launch_kv_merge<16>(a, st);
+    return e != cudaSuccess ? e : launch_merge<16>(a, st);
 }
 
 }  // namespace bsa

@@ -35,6 +35,7 @@ struct AttnArgs {
     float* part;               // partial results: [teams][2][R][M] rows of 64 + 1 floats
     int* desc;                 // [teams] records of kDesc ints: the item a team leaves unfinished
     int max_teams, R;          // R blocks of a team walk the same keys, each for its own query tile
+    int mr;                    // rows of a query tile (at most the M of its kernel)
     int min_run;               // fewest units worth a team of its own
     int32_t* status;
 };
@@ -92,22 +93,23 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& q, int i0,
 }
 __device__ __forceinline__ int unit_of(const Span& s, int j) { return j < s.n_sink ? j : s.t_lo + (j - s.n_sink); }
 
-// Work is counted in units of 128 keys. An item is one row group (R query tiles of M rows; a
+// Work is counted in units of 128 keys. An item is one row group (R query tiles of mr rows; a
 // row is one query head of one token, the heads of a group next to each other) of one key/value
 // head, with at least one unit, so that rows that see nothing are written too. The units of all
 // items in the order sequence, head, row group are dealt out to the teams in equal runs: a team
 // finishes the items that lie inside its run and leaves partial results of the (at most two)
 // that cross its ends, which the merge kernel joins in a fixed order.
-template <int M>
 __device__ __forceinline__ int group_count(const AttnArgs& a, const Seq& q) {
-    const int tiles = (q.n * a.group + M - 1) / M;
+    const int tiles = (q.n * a.group + a.mr - 1) / a.mr;
     return (tiles + a.R - 1) / a.R;
 }
-template <int M>
+// rows [r0, r1) of a sequence's chunk
+__device__ __forceinline__ Span rows_span(const AttnArgs& a, const Seq& q, int r0, int r1) {
+    return span_of(a, q, r0 / a.group, (min(r1, q.n * a.group) - 1) / a.group);
+}
 __device__ __forceinline__ Span group_span(const AttnArgs& a, const Seq& q, int rg) {
-    const int i0 = (int)((long long)rg * a.R * M / a.group);
-    const int i1 = (int)min((long long)q.n, ((long long)(rg + 1) * a.R * M + a.group - 1) / a.group) - 1;
-    return span_of(a, q, i0, i1);
+    const int r0 = rg * a.R * a.mr;
+    return rows_span(a, q, r0, r0 + a.R * a.mr);
 }
 
 struct Start {
@@ -121,7 +123,6 @@ __device__ __forceinline__ long long shfl_up64(long long v, int d) { return __sh
 
 // Fills pre[s] = units of sequences 0 .. s - 1 (pre[seqs] = total) and finds the item of the first
 // unit of a team. Whole block; `list` holds seqs + 1 ints. All in shared memory.
-template <int M>
 __device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre, int* list, Start* st) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int S = a.c.seqs;
@@ -129,12 +130,12 @@ __device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre
     __syncthreads();
     for (int s = tid; s < S; s += nt) {
         const Seq q = load_seq(a.c, a.cu, a.rows, s, a.status, blockIdx.x == 0);
-        const int ng = group_count<M>(a, q);
+        const int ng = group_count(a, q);
         long long u = 0;
         if (a.unit == 0) {
-            u = ng > 0 ? (long long)ng * max(1, group_span<M>(a, q, 0).count) : 0;
+            u = ng > 0 ? (long long)ng * max(1, group_span(a, q, 0).count) : 0;
         } else if (ng <= 8) {
-            for (int g = 0; g < ng; ++g) u += max(1, group_span<M>(a, q, g).count);
+            for (int g = 0; g < ng; ++g) u += max(1, group_span(a, q, g).count);
         } else {
             list[atomicAdd(&list[S], 1)] = s;   // long chunks: one warp each, below
         }
@@ -144,9 +145,9 @@ __device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre
     for (int x = warp; x < list[S]; x += nw) {
         const int s = list[x];
         const Seq q = load_seq(a.c, a.cu, a.rows, s, nullptr, false);
-        const int ng = group_count<M>(a, q);
+        const int ng = group_count(a, q);
         long long u = 0;
-        for (int g = lane; g < ng; g += 32) u += max(1, group_span<M>(a, q, g).count);
+        for (int g = lane; g < ng; g += 32) u += max(1, group_span(a, q, g).count);
         for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
         if (lane == 0) pre[s] = u * a.c.kv_heads;
     }
@@ -184,9 +185,9 @@ __device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre
             r.h = (int)(off / per_head);
             r.item += (long long)r.h * per_head;
             long long rest = off - (long long)r.h * per_head;
-            const int ng = group_count<M>(a, q);
+            const int ng = group_count(a, q);
             for (int g0 = 0; g0 < ng; g0 += 32) {
-                const long long own = g0 + lane < ng ? max(1, group_span<M>(a, q, g0 + lane).count) : 0;
+                const long long own = g0 + lane < ng ? max(1, group_span(a, q, g0 + lane).count) : 0;
                 long long v = own;
                 for (int d = 1; d < 32; d <<= 1) {
                     const long long o = shfl_up64(v, d);
@@ -211,7 +212,6 @@ __device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre
 
 // Walks the segments (item, run of its units) of one team. Every role of a block runs its own
 // copy over the same tables.
-template <int M>
 struct Walk {
     const AttnArgs& a;
     long long u, u1, item;     // next unit, end of the team's run, first unit of the item
@@ -235,7 +235,7 @@ struct Walk {
     }
     __device__ __forceinline__ void enter() {
         q = load_seq(a.c, a.cu, a.rows, s, nullptr, false);
-        ng = group_count<M>(a, q);
+        ng = group_count(a, q);
     }
     // the next segment; false when the run is done
     __device__ __forceinline__ bool next() {
@@ -248,7 +248,7 @@ struct Walk {
                 enter();
             }
         }
-        span = group_span<M>(a, q, rg);
+        span = group_span(a, q, rg);
         const int cnt = max(1, span.count);
         j0 = (int)(u - item);
         j1 = (int)(min(item + cnt, u1) - item);

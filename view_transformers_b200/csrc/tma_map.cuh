@@ -44,4 +44,20 @@ inline bool make_tile_map(CUtensorMap* tm, const void* base, uint64_t rows, uint
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map over heads x tokens of a bf16 tensor [tokens, heads, 64] with `stride` elements between
+// tokens: a box is 64 columns x `heads_box` heads x `tokens_box` tokens, the heads of one token
+// next to each other. Tokens past the end read zeros.
+inline bool make_rows_map(CUtensorMap* tm, const void* base, uint64_t tokens, uint64_t heads, uint64_t stride,
+                          uint32_t heads_box, uint32_t tokens_box) {
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr || tokens == 0) return false;
+    cuuint64_t dims[3] = {64, heads, tokens};
+    cuuint64_t strides[2] = {128, stride * 2};
+    cuuint32_t box[3] = {64, heads_box, tokens_box};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace bsa
