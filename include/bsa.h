@@ -378,8 +378,8 @@ BSA_API bsa_status bsa_attention_noalloc(const bsa_layout* layout, const void* q
  * through status_dev and their accesses skipped. Rows of a page that several sequences share
  * may be read by all of them; two rows appended to one place in one call are a race.
  * Limits (BSA_ERR_UNSUPPORTED): head_dim 64; page_tokens 16, 32, 64, 128 or 256; seqs <=
- * BSA_KV_MAX_SEQS; heads <= BSA_MAX_HEADS; pages * kv_heads * page_tokens, max_pages *
- * page_tokens, rows * heads < 2^31.
+ * BSA_KV_MAX_SEQS; heads <= BSA_MAX_HEADS; pages * kv_heads * page_tokens and max_pages *
+ * page_tokens < 2^31; rows * heads < 2^30; row strides <= 2^38.
  */
 #define BSA_KV_MAX_SEQS 1024
 typedef enum { BSA_KV_BF16 = 0, BSA_KV_E4M3 = 1 } bsa_kv_format;
@@ -437,7 +437,9 @@ BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const in
  *   lse       : device, float32 [heads, rows], or NULL
  *   workspace : device, 16-byte aligned, bsa_kv_workspace_size() bytes; needs no clearing and
  *               keeps nothing between calls; calls that may overlap need one each
- * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product. */
+ * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product. A call
+ * whose work exceeds 2^25 pairs of a query tile (8 to 128 rows) and 128 keys in one sequence is
+ * refused as BSA_ERR_UNSUPPORTED through status_dev. */
 BSA_API bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max_new, int32_t unit,
                                     int32_t window, int32_t sink, const int32_t* cu_new, const void* q,
                                     int64_t q_stride, void* out, int64_t out_stride, float* lse, void* workspace,

@@ -9,7 +9,7 @@ cudaError_t launch_kv_copy(const kv::CacheArgs& c, bool fp8, bool read, int rows
                            const int32_t* first, const void* const src[2], void* const dst[2],
                            uint8_t* const scale[2], long long stride, int32_t* status, cudaStream_t st);
 cudaError_t launch_kv_rows(kv::AttnArgs& a, bool fp8, bool eight, cudaStream_t st);
-cudaError_t launch_kv_tc(kv::AttnArgs& a, bool fp8, cudaStream_t st);
+cudaError_t launch_kv_tc(kv::AttnArgs& a, bool fp8, int max_new, cudaStream_t st);
 
 namespace {
 
@@ -40,7 +40,7 @@ bsa_status check_cache(const bsa_kv_cache* c, int32_t rows, kv::CacheArgs* a) {
     const bsa_status s = check_sizes(c);
     if (s != BSA_OK) return s;
     if (rows < 0) return BSA_ERR_INVALID_ARG;
-    if ((int64_t)rows * c->heads > kMost) return BSA_ERR_UNSUPPORTED;
+    if ((int64_t)rows * c->heads > kMost / 2) return BSA_ERR_UNSUPPORTED;
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !c->page_table || !aligned4(c->page_table) ||
         !c->kv_len || !aligned4(c->kv_len))
         return BSA_ERR_INVALID_ARG;
@@ -155,11 +155,10 @@ bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + desc_bytes());
     a.status = status_dev;
     a.max_teams = max_blocks();
-    a.R = 1;
     const bool fp8 = cache->format == BSA_KV_E4M3;
     const long long per_head = (long long)max_new * a.group;   // query rows of a key/value head, at most
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return from_cuda(per_head > 16 ? launch_kv_tc(a, fp8, st) : launch_kv_rows(a, fp8, per_head <= 8, st));
+    return from_cuda(per_head > 16 ? launch_kv_tc(a, fp8, max_new, st) : launch_kv_rows(a, fp8, per_head <= 8, st));
 }
 
 }  // extern "C"

@@ -120,31 +120,43 @@ kv_rows_kernel(const AttnArgs a) {
     const int g = lane >> 2, t = lane & 3;
     const int team = blockIdx.x;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < M * 2) (&poison[0][0])[tid] = 0u;
-    plan(a, team, reinterpret_cast<long long*>(smem),
-            reinterpret_cast<int*>(smem + sizeof(long long) * (BSA_KV_MAX_SEQS + 1)), &start);
-    const Start st = start;
+    let_next_start();
+    wait_for_previous();
+    int* tables = reinterpret_cast<int*>(smem);
+    const Start st = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &start);
     if (tid == 0) a.desc[team * kDesc] = 0;
-    if (team >= st.teams) return;
+    if (team >= st.teams || st.total == 0) return;
+    __syncthreads();
 
     const uint32_t ring = sm100::smem_u32(smem) + warp * (C::kStages * C::kStepBytes);
     float* mo = reinterpret_cast<float*>(smem + C::kRing);            // [warp][row][64]
     float* mml = mo + kWarps * M * 64;                                // [warp][row][2]
 
-    // the loader runs kStages - 1 steps ahead of the arithmetic, across items
+    // the loader runs kStages - 1 steps ahead of the arithmetic, across items; lane i holds the
+    // page of the unit lbase + i of the loader's segment
     Walk lw(a, st, team);
     bool live = lw.next();
-    int lj = live ? lw.j0 : 0;
+    int lj = live ? lw.j0 : 0, lbase = lj - 32, lpage = -1;
     uint32_t held = 0u;                     // bit s: stage s holds keys
     auto load_step = [&](int stage) {
         bool ok = false;
         if (live) {
-            const int kb = unit_of(lw.span, lj) * kUnit + warp * 16;
-            if (kb < lw.span.hi_max && (kb + 16 > lw.span.lo_min || kb < a.sink)) {
-                const int page = a.c.table[(long long)lw.s * a.c.max_pages + (kb >> a.c.pshift)];
-                ok = page >= 0 && page < a.c.pages;
-                if (page >= a.c.pages && lane == 0) record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
+            if (lj - lbase >= 32) {
+                lbase = lj;
+                lpage = -1;
+                const int k = unit_of(lw.span, lj + lane) * kUnit + warp * 16;
+                if (lj + lane < lw.j1 && k < lw.span.hi_max && (k + 16 > lw.span.lo_min || k < a.sink))
+                    lpage = a.c.table[(long long)lw.s * a.c.max_pages + (k >> a.c.pshift)];
+                if (lpage >= a.c.pages) {
+                    record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
+                    lpage = -1;
+                }
+            }
+            const int page = __shfl_sync(0xffffffffu, lpage, lj - lbase);
+            ok = page >= 0;
+            {
+                const int kb = unit_of(lw.span, lj) * kUnit + warp * 16;
                 if (ok) {
                     const long long row =
                         (((long long)page * a.c.kv_heads + lw.h) << a.c.pshift) + (kb & ((1 << a.c.pshift) - 1));
@@ -181,6 +193,7 @@ kv_rows_kernel(const AttnArgs a) {
                 lw.done();
                 live = lw.next();
                 lj = live ? lw.j0 : 0;
+                lbase = lj - 32;
             }
         }
         held = (held & ~(1u << stage)) | ((ok ? 1u : 0u) << stage);
@@ -504,7 +517,7 @@ kv_rows_kernel(const AttnArgs a) {
             d[2] = q.n;
             d[3] = w.h;
             d[4] = w.rg;
-            d[5] = w.last_team(w.item + max(1, w.span.count), st.total);
+            d[5] = st.team_of(w.item + max(1, w.span.count) - 1);
             d[0] = 1;
         }
         __syncthreads();
@@ -516,42 +529,79 @@ kv_rows_kernel(const AttnArgs a) {
 
 // Joins the partial results of an item that crosses team ends: the team that holds its first
 // unit left it in run 1, the following ones in run 0. L = ln sum e^lse, out = sum e^(lse - L) o,
-// in the order of the teams. One block per (team, member).
+// in an order that only the split decides. One block per 16 rows of a (team, member); 16 threads
+// hold a row's columns, and with fewer rows several sets of 16 share a row's pieces.
+constexpr int kMergeRows = 16;
 template <int M>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kMergeRows * 16)
 kv_merge_kernel(const AttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float4 sacc[kMergeRows][16];
+    __shared__ float2 sml[kMergeRows][16];
+    let_next_start();
+    wait_for_previous();
     const int team = blockIdx.x / a.R, member = blockIdx.x - team * a.R;
     const int* d = a.desc + team * kDesc;
     if (d[0] == 0) return;
-    const int row0 = d[1], n = d[2], h = d[3], last = d[5];
-    const long long r0 = ((long long)d[4] * a.R + member) * a.mr;
-    const int nrows = (int)min((long long)a.mr, (long long)n * a.group - r0);
-    const int c4 = (threadIdx.x & 15) * 4;
-    for (int r = threadIdx.x >> 4; r < nrows; r += 16) {
-        float mx = part_at<M>(a, team, 1, member)[M * 64 + r];
-        for (int k = team + 1; k <= last; ++k) mx = fmaxf(mx, part_at<M>(a, k, 0, member)[M * 64 + r]);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll 4
-        for (int k = team; k <= last; ++k) {
-            const float* p = part_at<M>(a, k, k == team ? 1 : 0, member);
-            const float e = p[M * 64 + r];
-            const float f = e == -INFINITY ? 0.f : ex2_approx((e - mx) * 1.4426950408889634f);
-            const float4 v = *reinterpret_cast<const float4*>(p + r * 64 + c4);
-            sum += f;
-            acc[0] += f * v.x;
-            acc[1] += f * v.y;
-            acc[2] += f * v.z;
-            acc[3] += f * v.w;
+    const int row0 = d[1], h = d[3], last = d[5];
+    const int r0 = (d[4] * a.R + member) * a.mr, rb = blockIdx.y * kMergeRows;
+    const int nrows = min(min(a.mr, d[2] * a.group - r0) - rb, kMergeRows);
+    if (nrows <= 0) return;
+    int sets = 1;                                // sets of 16 threads per row: a power of two
+    while (nrows * sets * 2 <= kMergeRows) sets *= 2;
+    const int c = threadIdx.x & 15, slot = threadIdx.x >> 4, r = slot / sets, set = slot - r * sets;
+    float m = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nrows) {
+        constexpr int U = 4;
+        for (int k = team + set; k <= last; k += U * sets) {
+            float e[U];
+            float4 v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int kk = min(k + i * sets, last);
+                const float* p = part_at<M>(a, kk, kk == team ? 1 : 0, member) + (rb + r) * 64;
+                v[i] = *reinterpret_cast<const float4*>(p + 4 * c);
+                e[i] = part_at<M>(a, kk, kk == team ? 1 : 0, member)[M * 64 + rb + r] * 1.4426950408889634f;
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (k + i * sets > last || e[i] == -INFINITY) continue;
+                const float n = fmaxf(m, e[i]), f0 = ex2_approx(m - n), f1 = ex2_approx(e[i] - n);
+                m = n;
+                sum = sum * f0 + f1;
+                acc.x = acc.x * f0 + v[i].x * f1;
+                acc.y = acc.y * f0 + v[i].y * f1;
+                acc.z = acc.z * f0 + v[i].z * f1;
+                acc.w = acc.w * f0 + v[i].w * f1;
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int i = (int)(r0 + r) / a.group;
-        const int head = h * a.group + (int)(r0 + r - (long long)i * a.group);
-        *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + c4) =
-            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-        if (c4 == 0 && a.lse != nullptr)
-            a.lse[(long long)head * a.rows + row0 + i] = sum == 0.f ? -INFINITY : mx + logf(sum);
     }
+    if (sets > 1) {
+        sacc[slot][c] = acc;
+        sml[slot][c] = make_float2(m, sum);
+        __syncthreads();
+        if (set != 0 || r >= nrows) return;
+        for (int k = 1; k < sets; ++k) {
+            const float2 o = sml[slot + k][c];
+            const float4 v = sacc[slot + k][c];
+            if (o.x == -INFINITY) continue;
+            const float n = fmaxf(m, o.x), f0 = ex2_approx(m - n), f1 = ex2_approx(o.x - n);
+            m = n;
+            sum = sum * f0 + o.y * f1;
+            acc.x = acc.x * f0 + v.x * f1;
+            acc.y = acc.y * f0 + v.y * f1;
+            acc.z = acc.z * f0 + v.z * f1;
+            acc.w = acc.w * f0 + v.w * f1;
+        }
+    }
+    if (r >= nrows) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i = (r0 + rb + r) / a.group;
+    const int head = h * a.group + (r0 + rb + r - i * a.group);
+    *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + 4 * c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (c == 0 && a.lse != nullptr)
+        a.lse[(long long)head * a.rows + row0 + i] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 template <bool FP8, int M>
@@ -560,24 +610,15 @@ cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
     auto kern = kv_rows_kernel<FP8, M>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<a.max_teams, kThreads, C::kSmem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(a.max_teams), kThreads, C::kSmem, st, a);
 }
 
 }  // namespace
 
 template <int M>
 static cudaError_t launch_merge(const AttnArgs& a, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.max_teams * a.R);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_merge_kernel<M>, a);
+    return launch_early(kv_merge_kernel<M>, dim3(a.max_teams * a.R, (a.mr + kMergeRows - 1) / kMergeRows), kMergeRows * 16,
+                        0, st, a);
 }
 
 cudaError_t launch_kv_merge128(const AttnArgs& a, cudaStream_t st) { return launch_merge<128>(a, st); }

@@ -52,13 +52,27 @@ struct Cfg {
     static constexpr uint32_t kOffCtl = kOffRaw + (FP8 ? kRaw * kRawHalf : 0);
 };
 
+// What the softmax has to know of a segment.
+struct Rec {
+    int tiles;             // key tiles to come (0: nothing to see); negative: no further segment
+    int nrows, r0;         // rows of the query tile, first one within the chunk
+    int row0, pos0, len;   // packed row and position of the chunk's first token, cached tokens
+    int h, whole, run;     // key/value head; the segment is the whole item; run of the partial result
+    int lo_min, hi_max;    // positions outside the sink that some row sees
+};
+
+// Per key tile: page mask (a bit per 16 keys) and these.
+enum { kFull = 0x100, kFirst = 0x200, kLast = 0x400, kEnd = 0x800 };
+
 struct Ctl {
     uint64_t q_full, q_empty;
     uint64_t k_full[3], kv_empty[3], v_full[3];      // v_full: e4m3 only (bf16: with k_full)
     uint64_t raw_full[kRaw], raw_empty[kRaw];
+    uint64_t rec_full[2], rec_empty[2];
     uint64_t s_full, s_free, p_full, o_done, o_final, drain;
-    int meta[3];                                     // page mask of the stage's tile
-    int raw_meta[kRaw];
+    Rec rec[2];
+    int meta[3], tile[3];                            // of the stages
+    int raw_meta[kRaw], raw_tile[kRaw];
     uint32_t tmem_base;
     int abort;
     Start start;
@@ -67,30 +81,6 @@ struct Ctl {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
-
-// This block's query tile within a segment, and the tiles of the segment's run that it needs.
-struct Mine {
-    const AttnArgs& a;
-    const Walk& w;
-    int r0, nrows;         // first row within the chunk; rows (0: nothing to do)
-    Span own;
-    int j;
-    __device__ __forceinline__ Mine(const AttnArgs& args, const Walk& walk, int member) : a(args), w(walk) {
-        r0 = (w.rg * a.R + member) * a.mr;
-        nrows = min(a.mr, w.q.n * a.group - r0);
-        if (nrows > 0) own = rows_span(a, w.q, r0, r0 + a.mr);
-        j = w.j0;
-    }
-    // next key tile; false at the end of the run
-    __device__ __forceinline__ bool next(int& t) {
-        while (j < w.j1) {
-            t = unit_of(w.span, j++);
-            const int k0 = t * kUnit;
-            if (k0 < own.hi_max && (k0 + kUnit > own.lo_min || k0 < a.sink)) return true;
-        }
-        return false;
-    }
-};
 
 // low n bits, any n
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -123,7 +113,8 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int team = blockIdx.x / a.R, member = blockIdx.x - team * a.R;
     volatile int* abort = &ctl.abort;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
 
     if (threadIdx.x == 0 && member == 0) a.desc[team * kDesc] = 0;
     // tile swizzles assume a 1024-byte aligned base; refuse to run otherwise
@@ -131,10 +122,9 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (threadIdx.x == 0) record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
         return;
     }
-    plan(a, team, reinterpret_cast<long long*>(smem),
-         reinterpret_cast<int*>(smem + sizeof(long long) * (BSA_KV_MAX_SEQS + 1)), &ctl.start);
-    const Start start = ctl.start;
-    if (team >= start.teams) return;
+    int* tables = reinterpret_cast<int*>(smem);
+    const Start start = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &ctl.start);
+    if (team >= start.teams || start.total == 0) return;
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 1);
         mbar_init(&ctl.q_empty, 1);
@@ -146,6 +136,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&ctl.raw_full[s], 1);
             mbar_init(&ctl.raw_empty[s], 2);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl.rec_full[s], 1);
+            mbar_init(&ctl.rec_empty[s], 4);
         }
         mbar_init(&ctl.s_full, 1);
         mbar_init(&ctl.s_free, 4);
@@ -179,37 +173,89 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (warp == 0) {
             // ======================================================== producer
             const int box = min(1 << a.c.pshift, 128), shift = min(a.c.pshift, 7);   // keys of a TMA box
-            int U = 0, I = 0;
+            int U = 0, I = 0, X = 0;     // tiles, Q tiles, segments so far
             bool ok = true;
             Walk w(a, start, team);
+            auto put_record = [&](const Rec& r) -> bool {
+                const int slot = X & 1;
+                if (X >= 2 && !warp_wait(&ctl.rec_empty[slot], ((X >> 1) - 1) & 1, abort, a.status)) return false;
+                if (lane == 0) {
+                    ctl.rec[slot] = r;
+                    mbar_arrive(&ctl.rec_full[slot]);
+                }
+                ++X;
+                return true;
+            };
             while (ok && w.next()) {
-                Mine mine(a, w, member);
-                int t;
-                if (mine.nrows <= 0 || !mine.next(t)) {
+                const int r0 = (w.rg * a.R + member) * a.mr;
+                const int nrows = min(a.mr, w.q.n * a.group - r0);
+                if (nrows <= 0) {
                     w.done();
                     continue;
                 }
-                if (I > 0 && !warp_wait(&ctl.q_empty, (I - 1) & 1, abort, a.status)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&ctl.q_full, a.mr * 128);
-                    tma_load_3d(smem + C::kOffQ, &tm_q, &ctl.q_full, 0, w.h * a.group, w.q.row0 + mine.r0 / a.group);
+                const Span own = rows_span(a, w.q, r0, r0 + a.mr);
+                auto wanted = [&](int k0, int n) { return k0 < own.hi_max && (k0 + n > own.lo_min || k0 < a.sink); };
+                // how many of the run's tiles this query tile needs: of the tiles [0, sinks) and
+                // [lo, hi) those that the run's two stretches (unit_of) hold
+                const int hi = (own.hi_max + kUnit - 1) / kUnit, lo = own.lo_min / kUnit;
+                const int sinks = min(min((int)(((long long)a.sink + kUnit - 1) / kUnit), lo), hi);
+                auto held = [&](int p, int q) {
+                    return max(0, min(q, sinks) - p) + max(0, min(q, hi) - max(p, lo));
+                };
+                const int skip = w.span.t_lo - w.span.n_sink;
+                const int tiles = held(w.j0, min(w.j1, w.span.n_sink)) + held(max(w.j0, w.span.n_sink) + skip, w.j1 + skip);
+                Rec rec;
+                rec.tiles = tiles;
+                rec.nrows = nrows;
+                rec.r0 = r0;
+                rec.row0 = w.q.row0;
+                rec.pos0 = w.q.len - w.q.n;
+                rec.len = w.q.len;
+                rec.h = w.h;
+                rec.whole = w.has_start && w.has_end;
+                rec.run = w.has_start ? 1 : 0;
+                rec.lo_min = own.lo_min;
+                rec.hi_max = own.hi_max;
+                if (!put_record(rec)) break;
+                if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
+                    int* d = a.desc + team * kDesc;
+                    d[1] = w.q.row0;
+                    d[2] = w.q.n;
+                    d[3] = w.h;
+                    d[4] = w.rg;
+                    d[5] = start.team_of(w.item + max(1, w.span.count) - 1);
+                    d[0] = 1;
                 }
-                q_loads = ++I;
-                do {
+                if (tiles > 0) {
+                    if (I > 0 && !warp_wait(&ctl.q_empty, (I - 1) & 1, abort, a.status)) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&ctl.q_full, a.mr * 128);
+                        tma_load_3d(smem + C::kOffQ, &tm_q, &ctl.q_full, 0, w.h * a.group, w.q.row0 + r0 / a.group);
+                    }
+                    q_loads = ++I;
+                }
+                int left = tiles;
+                for (int j = w.j0; left > 0 && j < w.j1; ++j) {
+                    const int t = unit_of(w.span, j);
+                    if (!wanted(t * kUnit, kUnit)) continue;
                     // the pages of the tile, one box per lane
                     const int k0 = t * kUnit + lane * box;
                     int page = -1;
-                    if (lane < (128 >> shift) && k0 < mine.own.hi_max &&
-                        (k0 + box > mine.own.lo_min || k0 < a.sink))
+                    if (lane < (128 >> shift) && wanted(k0, box))
                         page = a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)];
                     if (page >= a.c.pages) {
                         record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
                         page = -1;
                     }
                     const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
-                    int meta = 0;
+                    int meta = (left == tiles ? kFirst : 0) | (left == 1 ? kLast : 0);
+                    --left;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) meta |= ((have >> ((i * 16) >> shift)) & 1u) << i;
+                    const int key = t * kUnit;
+                    if ((meta & 0xff) == 0xff && key + kUnit <= own.hi_min &&
+                        (key >= own.lo_max || key + kUnit <= min(a.sink, own.lo_min)))
+                        meta |= kFull;
                     const long long row = page < 0 ? 0
                         : (((long long)page * a.c.kv_heads + w.h) << a.c.pshift) + (k0 & ((1 << a.c.pshift) - 1));
                     const uint32_t at = lane * box;
@@ -221,6 +267,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         }
                         if (lane == 0) {
                             ctl.meta[st] = meta;
+                            ctl.tile[st] = t;
                             mbar_arrive_expect_tx(&ctl.k_full[st], __popc(have) * box * 256);
                         }
                         __syncwarp();
@@ -240,6 +287,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             uint8_t* dst = smem + C::kOffRaw + slot * kRawHalf;
                             if (lane == 0) {
                                 ctl.raw_meta[slot] = meta;
+                                ctl.raw_tile[slot] = t;
                                 mbar_arrive_expect_tx(&ctl.raw_full[slot], __popc(have) * box * 65);
                             }
                             __syncwarp();
@@ -253,8 +301,27 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (!ok) break;
                     }
                     ++U;
-                } while (mine.next(t));
+                }
                 w.done();
+            }
+            // no further tile, no further segment
+            if (ok && !*abort) {
+                const int st = U % NS, x = 2 * U, slot = x % kRaw;
+                if (!FP8 ? U < NS || warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)
+                         : x < kRaw || warp_wait(&ctl.raw_empty[slot], ((x / kRaw) - 1) & 1, abort, a.status)) {
+                    if (lane == 0) {
+                        if (FP8) {
+                            ctl.raw_meta[slot] = kEnd;
+                            mbar_arrive(&ctl.raw_full[slot]);
+                        } else {
+                            ctl.meta[st] = kEnd;
+                            mbar_arrive(&ctl.k_full[st]);
+                        }
+                    }
+                    Rec rec = {};
+                    rec.tiles = -1;
+                    put_record(rec);
+                }
             }
         } else if (warp == 1) {
             // ======================================================== MMA issuer
@@ -262,63 +329,53 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 constexpr uint32_t idesc_qk = idesc_f16(128, 128, 1u, false);
                 constexpr uint32_t idesc_pv = idesc_f16(128, 64, 1u, true);
                 const uint32_t q_base = smem_u32(smem + C::kOffQ);
-                auto issue_qk = [&](int U) -> bool {
-                    const int st = U % NS;
-                    if (!mbar_wait(&ctl.k_full[st], (U / NS) & 1, abort, a.status)) return false;
-                    tc_fence_after();
-                    const uint32_t k_base = smem_u32(smem + C::kOffK + st * kTile);
+                auto issue_qk = [&](int U) {
+                    const uint32_t k_base = smem_u32(smem + C::kOffK + (U % NS) * kTile);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_ss(tmem + kColS, sdesc_sw128(q_base + 32 * ks, 16, 1024),
                                sdesc_sw128(k_base + 32 * ks, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
                     mma_commit(&ctl.s_full);
-                    return true;
                 };
-                int U = 0, I = 0;
-                bool ok = true;
-                Walk w(a, start, team);
-                while (ok && w.next()) {
-                    Mine mine(a, w, member);
-                    int t;
-                    if (mine.nrows <= 0 || !mine.next(t)) {
-                        w.done();
-                        continue;
-                    }
-                    if (!mbar_wait(&ctl.q_full, I & 1, abort, a.status)) break;
-                    // the previous item's last S has been read by the softmax
-                    if (U > 0 && !mbar_wait(&ctl.s_free, (U - 1) & 1, abort, a.status)) break;
-                    if (!issue_qk(U)) break;
-                    for (bool first = true, more = true; more; first = false, ++U) {
-                        more = mine.next(t);
-                        if (more) {
-                            if (!mbar_wait(&ctl.s_free, U & 1, abort, a.status) || !issue_qk(U + 1)) {
-                                ok = false;
-                                break;
-                            }
-                        } else {
-                            mma_commit(&ctl.q_empty);   // the item's last Q K^T is issued
-                        }
-                        const int st = U % NS;
-                        if (FP8 && !mbar_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!mbar_wait(&ctl.p_full, U & 1, abort, a.status)) {
-                            ok = false;
-                            break;
-                        }
+                int I = 0, meta = 0;
+                bool fresh = true;             // tile U starts a segment
+                for (int U = 0;; ++U) {
+                    const int st = U % NS;
+                    if (fresh) {                   // within a segment its QK^T is issued already
+                        if (!mbar_wait(&ctl.k_full[st], (U / NS) & 1, abort, a.status)) break;
+                        meta = ctl.meta[st];
+                        if (meta & kEnd) break;
+                        if (!mbar_wait(&ctl.q_full, I & 1, abort, a.status)) break;
+                        ++I;
+                        // the previous segment's last S has been read by the softmax
+                        if (U > 0 && !mbar_wait(&ctl.s_free, (U - 1) & 1, abort, a.status)) break;
                         tc_fence_after();
-                        const uint32_t v_base = smem_u32(smem + C::kOffV + st * kTile);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(tmem + kColO, tmem + kColP + 8 * ks, sdesc_sw128(v_base + 2048 * ks, 0, 1024), idesc_pv,
-                                   (!first || ks > 0) ? 1u : 0u);
-                        mma_commit(&ctl.kv_empty[st]);
-                        mma_commit(&ctl.o_done);
-                        if (!more) mma_commit(&ctl.o_final);
+                        issue_qk(U);
                     }
-                    ++I;
-                    w.done();
+                    const int cur = meta;
+                    fresh = (cur & kLast) != 0;
+                    if (!fresh) {
+                        const int sn = (U + 1) % NS;
+                        if (!mbar_wait(&ctl.s_free, U & 1, abort, a.status) ||
+                            !mbar_wait(&ctl.k_full[sn], ((U + 1) / NS) & 1, abort, a.status))
+                            break;
+                        tc_fence_after();
+                        issue_qk(U + 1);
+                        meta = ctl.meta[sn];
+                    } else {
+                        mma_commit(&ctl.q_empty);   // the segment's last Q K^T is issued
+                    }
+                    if (FP8 && !mbar_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) break;
+                    if (!mbar_wait(&ctl.p_full, U & 1, abort, a.status)) break;
+                    tc_fence_after();
+                    const uint32_t v_base = smem_u32(smem + C::kOffV + st * kTile);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tmem + kColO, tmem + kColP + 8 * ks, sdesc_sw128(v_base + 2048 * ks, 0, 1024), idesc_pv,
+                               (!(cur & kFirst) || ks > 0) ? 1u : 0u);
+                    mma_commit(&ctl.kv_empty[st]);
+                    mma_commit(&ctl.o_done);
+                    if (fresh) mma_commit(&ctl.o_final);
                 }
             }
         } else if (FP8) {
@@ -326,62 +383,55 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // four lanes share a row of 64 codes; each writes two 16-byte chunks of the swizzled
             // bf16 row. Rows of pages that do not exist are left as they are.
             const int cw = warp - 2;
-            int U = 0;
             bool ok = true;
-            Walk w(a, start, team);
-            while (ok && w.next()) {
-                Mine mine(a, w, member);
-                int t;
-                if (mine.nrows <= 0) {
-                    w.done();
-                    continue;
-                }
-                while (mine.next(t)) {
-                    const int st = U % NS;
-                    if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) {
+            for (int U = 0; ok; ++U) {
+                const int st = U % NS;
+                if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int x = 2 * U + half, slot = x % kRaw;
+                    if (!warp_wait(&ctl.raw_full[slot], (x / kRaw) & 1, abort, a.status)) {
                         ok = false;
                         break;
                     }
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const int x = 2 * U + half, slot = x % kRaw;
-                        if (!warp_wait(&ctl.raw_full[slot], (x / kRaw) & 1, abort, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint8_t* src = smem + C::kOffRaw + slot * kRawHalf;
-                        uint8_t* dst = smem + (half ? C::kOffV : C::kOffK) + st * kTile;
-                        const int meta = ctl.raw_meta[slot];
-                        if (cw == 0 && lane == 0 && half == 0) ctl.meta[st] = meta;
-#pragma unroll 4
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = i * 16 + cw * 8 + (lane >> 2);
-                            if ((meta >> i) & 1) {
-                                const uint4 c = *reinterpret_cast<const uint4*>(src + r * 64 + (lane & 3) * 16);
-                                const uint32_t b = src[8192 + r];
-                                // 2^(b - 127 + 112); bytes above 142 (255, or never written): NaN
-                                const uint32_t f1 = b > 142u ? 0x7fc0u : (b + 112u) << 7, f2 = f1 | (f1 << 16);
-                                const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&f2);
-                                const int c0 = 2 * (lane & 3);
-                                *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) * 16)) =
-                                    make_uint4(bf16_of(c.x, false, f), bf16_of(c.x, true, f), bf16_of(c.y, false, f),
-                                               bf16_of(c.y, true, f));
-                                *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) * 16)) =
-                                    make_uint4(bf16_of(c.z, false, f), bf16_of(c.z, true, f), bf16_of(c.w, false, f),
-                                               bf16_of(c.w, true, f));
-                            }
-                        }
-                        fence_async_shared();
+                    const uint8_t* src = smem + C::kOffRaw + slot * kRawHalf;
+                    uint8_t* dst = smem + (half ? C::kOffV : C::kOffK) + st * kTile;
+                    const int meta = ctl.raw_meta[slot];
+                    if (cw == 0 && lane == 0 && half == 0) {
+                        ctl.meta[st] = meta;
+                        ctl.tile[st] = ctl.raw_tile[slot];
+                    }
+                    if (meta & kEnd) {
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(half ? &ctl.v_full[st] : &ctl.k_full[st]);
-                            mbar_arrive(&ctl.raw_empty[slot]);
+                        if (lane == 0) mbar_arrive(&ctl.k_full[st]);
+                        ok = false;
+                        break;
+                    }
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 16 + cw * 8 + (lane >> 2);
+                        if ((meta >> i) & 1) {
+                            const uint4 c = *reinterpret_cast<const uint4*>(src + r * 64 + (lane & 3) * 16);
+                            const uint32_t b = src[8192 + r];
+                            // 2^(b - 127 + 112); bytes above 142 (255, or never written): NaN
+                            const uint32_t f1 = b > 142u ? 0x7fc0u : (b + 112u) << 7, f2 = f1 | (f1 << 16);
+                            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&f2);
+                            const int c0 = 2 * (lane & 3);
+                            *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) * 16)) =
+                                make_uint4(bf16_of(c.x, false, f), bf16_of(c.x, true, f), bf16_of(c.y, false, f),
+                                           bf16_of(c.y, true, f));
+                            *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) * 16)) =
+                                make_uint4(bf16_of(c.z, false, f), bf16_of(c.z, true, f), bf16_of(c.w, false, f),
+                                           bf16_of(c.w, true, f));
                         }
                     }
-                    if (!ok) break;
-                    ++U;
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(half ? &ctl.v_full[st] : &ctl.k_full[st]);
+                        mbar_arrive(&ctl.raw_empty[slot]);
+                    }
                 }
-                w.done();
             }
         }
     } else {
@@ -391,21 +441,17 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         int U = 0, I = 0;
-        bool ok = true;
-        Walk w(a, start, team);
-        while (ok && w.next()) {
-            Mine mine(a, w, member);
-            if (mine.nrows <= 0) {
-                w.done();
-                continue;
-            }
+        for (int X = 0;; ++X) {
+            if (!warp_wait(&ctl.rec_full[X & 1], (X >> 1) & 1, abort, a.status)) break;
+            const Rec& rec = ctl.rec[X & 1];
+            const int tiles = rec.tiles;
+            if (tiles < 0) break;
             float m_ref = -INFINITY, l = 0.f;
             uint32_t poison0 = 0u, poison1 = 0u;   // columns that met a non-finite value of a key the row sees
             int lo = 0, hi = 0;
-            if (row < mine.nrows) visible(a, w.q.len, w.q.len - w.q.n + (mine.r0 + row) / a.group, lo, hi);
-            int t;
-            bool first = true;
-            while (mine.next(t)) {
+            if (row < rec.nrows) visible(a, rec.len, rec.pos0 + (rec.r0 + row) / a.group, lo, hi);
+            bool ok = true;
+            for (int u = 0; u < tiles; ++u, ++U) {
                 const int st = U % NS;
                 if (!warp_wait(&ctl.s_full, U & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
@@ -413,20 +459,16 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tmem_ld32(lane_base + kColS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
-                // done already (the product waited for it): orders the read of the page mask
+                // done already (the product waited for it): orders the read of the tile's words
                 if (!warp_wait(&ctl.k_full[st], (U / NS) & 1, abort, a.status)) { ok = false; break; }
                 const int meta = ctl.meta[st];
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.s_free);
-                const int k0 = t * kUnit;
-                const Span& own = mine.own;
-                const bool full = meta == 0xff && k0 + kUnit <= own.hi_min &&
-                                  (k0 >= own.lo_max || k0 + kUnit <= min(a.sink, own.lo_min));
                 float mt = -INFINITY;
                 uint32_t see[4];
-                if (full) {
+                if (meta & kFull) {
                     float acc[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) acc[i] = __uint_as_float(s[i]);
@@ -436,6 +478,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     mt = max3f(max3f(acc[0], acc[1], acc[2]), max3f(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
                 } else {
                     // columns of this row that count
+                    const int k0 = ctl.tile[st] * kUnit;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int b = k0 + 32 * k;
@@ -451,7 +494,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (FP8 && !warp_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) { ok = false; break; }
                     uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * kTile + row * 128);
                     const int key = k0 + row;
-                    const bool any = ((meta >> (row >> 4)) & 1) && key < own.hi_max && (key >= own.lo_min || key < a.sink);
+                    const bool any = ((meta >> (row >> 4)) & 1) && key < rec.hi_max && (key >= rec.lo_min || key < a.sink);
                     uint32_t bad0 = 0u, bad1 = 0u;
                     if (any) {
 #pragma unroll 1
@@ -525,7 +568,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 l = l * factor + rs;
                 // P.V of the item's previous tile must be done before O is rescaled or P is
                 // overwritten (for the first tile, the previous item's o_final wait covered it)
-                if (!first && !warp_wait(&ctl.o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
+                if (u > 0 && !warp_wait(&ctl.o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, corr)) {
 #pragma unroll
@@ -545,23 +588,21 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.p_full);
-                first = false;
-                ++U;
             }
             if (!ok) break;
             // -------------------------------------------------------- epilogue of the segment
-            const bool some = !first;
+            const bool some = tiles > 0;
             if (some) {
-                if (!warp_wait(&ctl.o_final, I & 1, abort, a.status)) { ok = false; break; }
+                if (!warp_wait(&ctl.o_final, I & 1, abort, a.status)) break;
                 tc_fence_after();
                 ++I;
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;   // l = 0: nothing seen. NaN stays.
             const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-            const bool whole = w.has_start && w.has_end;
-            const int i = (mine.r0 + row) / a.group;
-            const int head = w.h * a.group + (mine.r0 + row - i * a.group);
-            float* part = part_at<128>(a, team, w.has_start ? 1 : 0, member);
+            const bool whole = rec.whole;
+            const int i = (rec.r0 + row) / a.group;
+            const int head = rec.h * a.group + (rec.r0 + row - i * a.group);
+            float* part = part_at<128>(a, team, rec.run, member);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float o[32];
@@ -579,9 +620,9 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                     for (int c = 0; c < 32; ++c) o[c] = 0.f;
                 }
-                if (row < mine.nrows) {
+                if (row < rec.nrows) {
                     if (whole) {
-                        __nv_bfloat16* dst = a.out + (long long)(w.q.row0 + i) * a.out_stride + head * 64 + 32 * k;
+                        __nv_bfloat16* dst = a.out + (long long)(rec.row0 + i) * a.out_stride + head * 64 + 32 * k;
 #pragma unroll
                         for (int c = 0; c < 32; c += 8) Vec16<__nv_bfloat16>::store(dst + c, o + c);
                     } else {
@@ -591,21 +632,13 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     }
                 }
             }
-            if (row < mine.nrows) {
+            if (row < rec.nrows) {
                 if (!whole) part[128 * 64 + row] = lse;
-                else if (a.lse != nullptr) a.lse[(long long)head * a.rows + w.q.row0 + i] = lse;
+                else if (a.lse != nullptr) a.lse[(long long)head * a.rows + rec.row0 + i] = lse;
             }
             tc_fence_before();
-            if (row == 0 && member == 0 && !whole && w.has_start) {   // the merge kernel's record of this item
-                int* d = a.desc + team * kDesc;
-                d[1] = w.q.row0;
-                d[2] = w.q.n;
-                d[3] = w.h;
-                d[4] = w.rg;
-                d[5] = w.last_team(w.item + max(1, w.span.count), start.total);
-                d[0] = 1;
-            }
-            w.done();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.rec_empty[X & 1]);
         }
     }
 
@@ -638,18 +671,36 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, cons
     auto kern = kv_tc_kernel<FP8>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.max_teams * a.R, C::kThreads, smem, st>>>(q, k, v, a);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(a.max_teams * a.R), C::kThreads, smem, st, q, k, v, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_merge128(const AttnArgs& a, cudaStream_t st);
 
-cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, cudaStream_t st) {
+// Blocks per team. The R blocks of a team read the same keys at about the same time, so with
+// tiles query tiles per chunk the cache comes from HBM tiles / R times instead of tiles times;
+// against that stand the members without a tile in a chunk's last row group and the blocks left
+// over when R does not divide their number. The largest R within 4% of the best use of the
+// blocks; 1 for chunks of unequal lengths (max_new well above the mean), whose short ones would
+// leave members idle.
+static int team_size(const AttnArgs& a, int blocks, int max_new) {
+    const int tiles = (int)(((long long)max_new * a.group + a.mr - 1) / a.mr);
+    if (tiles < 2 || (long long)a.rows * 100 < (long long)a.c.seqs * max_new * 85) return 1;
+    int best = 1;
+    for (int r = 2; r <= 16 && r <= tiles; ++r) {
+        const double use = (double)tiles / ((tiles + r - 1) / r * r) * (blocks / r * r) / blocks;
+        if (use >= 0.96) best = r;   // R = 1 uses all of them
+    }
+    return best;
+}
+
+cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
     const uint32_t tokens = 128 / a.group;
     a.mr = (int)tokens * a.group;
     a.min_run = 2;
+    a.R = team_size(a, a.max_teams, max_new);
+    a.max_teams /= a.R;
     const uint64_t rows = ((uint64_t)a.c.pages * a.c.kv_heads) << a.c.pshift;
     const uint32_t box = a.c.pshift < 7 ? 1u << a.c.pshift : 128u;
     CUtensorMap q, k, v;

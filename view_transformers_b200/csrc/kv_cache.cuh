@@ -114,117 +114,198 @@ __device__ __forceinline__ Span group_span(const AttnArgs& a, const Seq& q, int 
 
 struct Start {
     int s, h, rg;
-    int teams;         // teams that have work
-    long long item;    // first unit of the item
-    long long total;   // units of all items
+    int teams;                 // teams that have work
+    int item;                  // first unit of the item
+    int total;                 // units of all items
+    __device__ __forceinline__ int first_unit(int team) const {
+        const int q = total / teams, r = total - q * teams;
+        return q * team + min(team, r);
+    }
+    // the team that holds unit u
+    __device__ __forceinline__ int team_of(int u) const {
+        const int q = total / teams, r = total - q * teams, wide = r * (q + 1);
+        return u < wide ? u / (q + 1) : r + (u - wide) / q;
+    }
 };
 
-__device__ __forceinline__ long long shfl_up64(long long v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
+// inclusive sum over the lanes up to this one
+__device__ __forceinline__ int lane_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+__device__ __forceinline__ int lane_sum(int v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
 
-// Fills pre[s] = units of sequences 0 .. s - 1 (pre[seqs] = total) and finds the item of the first
-// unit of a team. Whole block; `list` holds seqs + 1 ints. All in shared memory.
-__device__ __forceinline__ void plan(const AttnArgs& a, int team, long long* pre, int* list, Start* st) {
+// Units of one key/value head of a sequence with few row groups (long: set instead).
+__device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q, bool& far) {
+    const int ng = group_count(a, q);
+    int u = 0;
+    if (a.unit == 0) {
+        u = ng > 0 ? ng * max(1, group_span(a, q, 0).count) : 0;
+    } else if (ng <= 4) {
+        for (int g = 0; g < ng; ++g) u += max(1, group_span(a, q, g).count);
+    } else {
+        far = true;
+    }
+    return u;
+}
+// the same of a sequence with many row groups, by a whole warp
+__device__ __forceinline__ int head_units_warp(const AttnArgs& a, const Seq& q, int lane) {
+    const int ng = group_count(a, q);
+    int u = 0;
+    for (int g = lane; g < ng; g += 32) u += max(1, group_span(a, q, g).count);
+    return lane_sum(u);
+}
+// teams that the total is worth, then the item of the first unit of `team`, which lies in
+// sequence r.s at unit `base` (whole warp)
+__device__ __forceinline__ void find_item(const AttnArgs& a, const Seq& q, int base, int per_head, int u0, int lane,
+                                          Start& r) {
+    r.h = (u0 - base) / per_head;
+    r.item = base + r.h * per_head;
+    r.rg = 0;
+    int rest = u0 - r.item;
+    const int ng = group_count(a, q);
+    if (a.unit == 0) {
+        const int each = per_head / ng;
+        r.rg = rest / each;
+        r.item += r.rg * each;
+        return;
+    }
+    for (int g0 = 0; g0 < ng; g0 += 32) {
+        const int own = g0 + lane < ng ? max(1, group_span(a, q, g0 + lane).count) : 0;
+        const int v = lane_scan(own, lane);
+        const unsigned in = __ballot_sync(0xffffffffu, g0 + lane < ng && rest < v);
+        if (in) {
+            const int at = __ffs(in) - 1;
+            r.rg = g0 + at;
+            r.item += __shfl_sync(0xffffffffu, v - own, at);
+            return;
+        }
+        const int all = __shfl_sync(0xffffffffu, v, 31);
+        rest -= all;
+        r.item += all;
+    }
+}
+
+constexpr int kMostUnits = 1 << 30;
+
+// The split of the work, for this block's team. Up to 32 sequences: every warp by itself,
+// without shared memory or a barrier. More: the whole block, through pre (seqs + 1 ints), list
+// (seqs + 1 ints) and *st in shared memory. Work beyond 2^30 units is refused.
+__device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int* list, Start* st) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int S = a.c.seqs;
+    Start r;
+    r.s = r.h = r.rg = r.item = 0;
+    if (S <= 32) {
+        Seq q;
+        q.row0 = q.n = q.len = 0;
+        if (lane < S) q = load_seq(a.c, a.cu, a.rows, lane, a.status, blockIdx.x == 0 && warp == 0);
+        bool far = false;
+        int u = head_units(a, q, far);
+        for (unsigned m = __ballot_sync(0xffffffffu, far); m; m &= m - 1) {
+            const int s = __ffs(m) - 1;
+            Seq o;
+            o.row0 = __shfl_sync(0xffffffffu, q.row0, s);
+            o.n = __shfl_sync(0xffffffffu, q.n, s);
+            o.len = __shfl_sync(0xffffffffu, q.len, s);
+            const int v = head_units_warp(a, o, lane);
+            if (lane == s) u = v;
+        }
+        const float most = (float)u * (float)a.c.kv_heads;   // 32 such sums stay inside 2^31
+        const bool over = __any_sync(0xffffffffu, most > (float)(kMostUnits / 32));
+        u *= a.c.kv_heads;
+        const int v = lane_scan(u, lane);
+        r.total = __shfl_sync(0xffffffffu, v, 31);
+        if (over) {
+            if (tid == 0) record_error(a.status, BSA_ERR_UNSUPPORTED);
+            r.total = 0;
+        }
+        r.teams = min(a.max_teams, max(1, r.total / a.min_run));
+        const int u0 = team < r.teams ? r.first_unit(team) : r.total;
+        const unsigned in = __ballot_sync(0xffffffffu, v > u0 && u > 0);
+        if (in && u0 < r.total) {
+            r.s = __ffs(in) - 1;
+            Seq o;
+            o.row0 = __shfl_sync(0xffffffffu, q.row0, r.s);
+            o.n = __shfl_sync(0xffffffffu, q.n, r.s);
+            o.len = __shfl_sync(0xffffffffu, q.len, r.s);
+            find_item(a, o, __shfl_sync(0xffffffffu, v - u, r.s), __shfl_sync(0xffffffffu, u, r.s) / a.c.kv_heads, u0, lane, r);
+        }
+        return r;
+    }
     if (tid == 0) list[S] = 0;
     __syncthreads();
     for (int s = tid; s < S; s += nt) {
         const Seq q = load_seq(a.c, a.cu, a.rows, s, a.status, blockIdx.x == 0);
-        const int ng = group_count(a, q);
-        long long u = 0;
-        if (a.unit == 0) {
-            u = ng > 0 ? (long long)ng * max(1, group_span(a, q, 0).count) : 0;
-        } else if (ng <= 8) {
-            for (int g = 0; g < ng; ++g) u += max(1, group_span(a, q, g).count);
-        } else {
-            list[atomicAdd(&list[S], 1)] = s;   // long chunks: one warp each, below
-        }
-        pre[s] = u * a.c.kv_heads;
+        bool far = false;
+        pre[s] = head_units(a, q, far);
+        if (far) list[atomicAdd(&list[S], 1)] = s;
     }
     __syncthreads();
     for (int x = warp; x < list[S]; x += nw) {
         const int s = list[x];
-        const Seq q = load_seq(a.c, a.cu, a.rows, s, nullptr, false);
-        const int ng = group_count(a, q);
-        long long u = 0;
-        for (int g = lane; g < ng; g += 32) u += max(1, group_span(a, q, g).count);
-        for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
-        if (lane == 0) pre[s] = u * a.c.kv_heads;
+        const int v = head_units_warp(a, load_seq(a.c, a.cu, a.rows, s, nullptr, false), lane);
+        if (lane == 0) pre[s] = v;
     }
     __syncthreads();
     if (warp == 0) {
-        long long base = 0;
+        int base = 0;
+        bool over = false;
         for (int s0 = 0; s0 < S; s0 += 32) {
-            const long long own = s0 + lane < S ? pre[s0 + lane] : 0;
-            long long v = own;
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long o = shfl_up64(v, d);
-                if (lane >= d) v += o;
-            }
+            const int per = s0 + lane < S ? pre[s0 + lane] : 0;
+            over |= (float)per * (float)a.c.kv_heads > (float)(kMostUnits / 32) || base > kMostUnits;
+            const int own = per * a.c.kv_heads;
+            const int v = lane_scan(own, lane);
             if (s0 + lane < S) pre[s0 + lane] = base + v - own;
             base += __shfl_sync(0xffffffffu, v, 31);
+            if (__any_sync(0xffffffffu, over)) break;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+            if (lane == 0) record_error(a.status, BSA_ERR_UNSUPPORTED);
+            base = 0;
         }
         if (lane == 0) pre[S] = base;
         __syncwarp();
-        Start r;
-        r.teams = (int)max(1ll, min((long long)a.max_teams, base / a.min_run));
-        const long long u0 = team < r.teams ? base * team / r.teams : base;
-        int lo = 0, hi = S;                     // last sequence with pre[s] <= u0 that has units
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= u0) lo = mid; else hi = mid;
-        }
-        r.s = lo;
         r.total = base;
-        r.h = r.rg = 0;
-        r.item = pre[lo];
+        r.teams = min(a.max_teams, max(1, base / a.min_run));
+        const int u0 = team < r.teams ? r.first_unit(team) : base;
         if (u0 < base) {
-            const Seq q = load_seq(a.c, a.cu, a.rows, lo, nullptr, false);
-            const long long per_head = (pre[lo + 1] - pre[lo]) / a.c.kv_heads;
-            const long long off = u0 - pre[lo];
-            r.h = (int)(off / per_head);
-            r.item += (long long)r.h * per_head;
-            long long rest = off - (long long)r.h * per_head;
-            const int ng = group_count(a, q);
-            for (int g0 = 0; g0 < ng; g0 += 32) {
-                const long long own = g0 + lane < ng ? max(1, group_span(a, q, g0 + lane).count) : 0;
-                long long v = own;
-                for (int d = 1; d < 32; d <<= 1) {
-                    const long long o = shfl_up64(v, d);
-                    if (lane >= d) v += o;
-                }
-                const unsigned in = __ballot_sync(0xffffffffu, g0 + lane < ng && rest < v);
-                if (in) {
-                    const int at = __ffs(in) - 1;
-                    r.rg = g0 + at;
-                    r.item += __shfl_sync(0xffffffffu, v - own, at);
-                    break;
-                }
-                const long long all = __shfl_sync(0xffffffffu, v, 31);
-                rest -= all;
-                r.item += all;
+            int lo = 0, hi = S;                     // the last sequence with pre[s] <= u0
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (pre[mid] <= u0) lo = mid; else hi = mid;
             }
+            r.s = lo;
+            find_item(a, load_seq(a.c, a.cu, a.rows, lo, nullptr, false), pre[lo], (pre[lo + 1] - pre[lo]) / a.c.kv_heads,
+                      u0, lane, r);
         }
         if (lane == 0) *st = r;
     }
     __syncthreads();
+    return *st;
 }
 
 // Walks the segments (item, run of its units) of one team. Every role of a block runs its own
 // copy over the same tables.
 struct Walk {
     const AttnArgs& a;
-    long long u, u1, item;     // next unit, end of the team's run, first unit of the item
+    int u, u1, item;           // next unit, end of the team's run, first unit of the item
     int s, h, rg, ng;
     Seq q;
     Span span;                 // of the whole row group
     int j0, j1;                // this segment's units within the item
     bool has_start, has_end;   // the segment holds the item's first, last unit
-    int teams;
     __device__ __forceinline__ Walk(const AttnArgs& args, const Start& st, int team) : a(args) {
-        teams = st.teams;
-        u = team < teams ? st.total * team / teams : st.total;
-        u1 = team < teams ? st.total * (team + 1) / teams : st.total;
+        u = team < st.teams ? st.first_unit(team) : st.total;
+        u1 = team < st.teams ? st.first_unit(team + 1) : st.total;
         item = st.item;
         s = st.s;
         h = st.h;
@@ -250,8 +331,8 @@ struct Walk {
         }
         span = group_span(a, q, rg);
         const int cnt = max(1, span.count);
-        j0 = (int)(u - item);
-        j1 = (int)(min(item + cnt, u1) - item);
+        j0 = u - item;
+        j1 = min(item + cnt, u1) - item;
         has_start = j0 == 0;
         has_end = j1 == cnt;
         return j1 > j0;        // false only if the tables changed under the call
@@ -264,13 +345,6 @@ struct Walk {
             ++rg;
         }
     }
-    // last team that holds units of the item that ends at unit `end`
-    __device__ __forceinline__ int last_team(long long end, long long total) const {
-        int t = (int)((end * teams + total - 1) / total) - 1;
-        while (t + 1 < teams && total * (t + 1) / teams < end) ++t;
-        while (t > 0 && total * t / teams >= end) --t;
-        return t;
-    }
 };
 
 // Where a block keeps the partial result of a segment: run 0 of a team for the item that
@@ -278,6 +352,26 @@ struct Walk {
 template <int M>
 __device__ __forceinline__ float* part_at(const AttnArgs& a, int team, int run, int member) {
     return a.part + ((long long)(team * 2 + run) * a.R + member) * (M * 65);
+}
+
+// Every kernel here is launched so that it may start while the one before it in the stream ends,
+// and waits for that one's results first.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
