@@ -132,6 +132,34 @@ def test_nan_of_a_later_token_stays_with_those_that_see_it(fmt, n):
     assert bool(torch.isnan(out[k:].float()).all())
 
 
+@pytest.mark.parametrize("n", [1, 12, 150])
+def test_small_values_beside_a_large_one_in_e4m3(n):
+    """One large element sets a row's scale and leaves the others among the subnormal codes."""
+    import torch
+    c = Case("small", (n,), (n + 300,), page=32, fmt="e4m3", unit=1)
+    x, host = tensors(c)
+    rng = np.random.default_rng(7)
+    table, P = x["table"].cpu().numpy(), c.page
+    for name in "kv":
+        rows = rng.uniform(-2.0 ** -6, 2.0 ** -6, host[name][0].shape)
+        rows[..., 11] = rng.choice([-400.0, 448.0], rows.shape[:-1])
+        if name == "k":
+            rows[..., 11] = 0.0
+            rows[..., 12] = 448.0
+        rows = bf16(rows * 2.0 ** rng.integers(-9, 2, rows.shape[:-1])[..., None])
+        vals, e = okv.quantise(rows)
+        host[name][0] = okv.dequantise(vals, e)
+        pos = np.arange(n + 300)
+        pg, slot = (torch.from_numpy(a).cuda() for a in (table[0, pos // P].astype(np.int64), pos % P))
+        x[name + "_pool"].view(torch.uint8)[pg, :, slot] = torch.from_numpy(vals).cuda().to(torch.float8_e4m3fn).view(torch.uint8)
+        x[name + "_scale"].view(torch.uint8)[pg, :, slot] = torch.from_numpy((e + 127).astype(np.uint8)).cuda()
+    x["q"][:, :, 12] = 0                                 # the large key element does not decide the scores
+    host["q"][0][:, :, 12] = 0
+    cache, out, lse = _attend(c, x)
+    assert cache.check_status() == 0
+    check_attention(out, lse, attention_oracle(c, host))
+
+
 def _fresh(c, device="cuda"):
     """A cache with its tables set, empty pools of a sentinel, and the new tokens."""
     import torch

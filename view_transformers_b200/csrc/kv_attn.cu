@@ -6,23 +6,24 @@
 //   keys a row sees, with a running reference m that is raised only when some x exceeds it by 8.
 //
 // With few rows the keys and values are read once and nothing else matters: the bound is HBM
-// (128 bytes a row of K or V, 65 in e4m3). So the matrix instruction is the small one, with
-// M rows (8 or 16 of its 16), and its operands go from HBM through a ring of asynchronous copies
-// straight into the registers that need them:
-//   - each warp takes 16 of the 128 keys of a unit and keeps its own m, l and O; the eight warps
-//     of a block meet at the end of an item;
+// (128 bytes a row of K or V, 65 in e4m3), and for e4m3 the instructions that turn codes into
+// operands. So the matrix instruction is the small one, with M rows (8 or 16 of its 16):
+//   - one warp gathers tiles of 128 keys from their pages by TMA into a ring of stages, running
+//     ahead across items; eight warps take 16 keys of each tile and keep their own m, l and O, and
+//     meet at the end of an item;
 //   - a dot product does not care about the order of its terms, so the lane that must hold two
 //     neighbouring d of key g takes 16 neighbouring bytes of that key instead, and Q is loaded in
-//     the same order; P.V's columns are likewise dealt out so that a lane needs 8 neighbouring d
-//     of four keys. Every lane then reads back only what it copied itself: no barrier, no bank
-//     conflict, and every copy covers whole 32-byte sectors;
+//     the same order; P.V's columns are dealt out so that a lane needs 8 neighbouring d of four
+//     keys. All reads of a stage are 8 or 16 bytes wide and free of bank conflicts: bf16 tiles are
+//     swizzled by TMA (16-byte chunk c of row r at c ^ (r & 7)); e4m3 tiles are not, and the keys
+//     are numbered so that the four rows that a lane quad needs lie next to each other;
 //   - e4m3 codes become f16 by one conversion for Q.K (Q is scaled to f16 per row, exact for
-//     elements within 2^-28 of the row's largest) and bf16 by shifting that for P.V, as powers of
-//     two away; the rows' scales go into the scores and into P, which bf16 holds without loss.
-#include <cfloat>
-
+//     elements within 2^-28 of the row's largest); for P.V their bits are moved into a bf16 as
+//     they are, 2^-120 times the value. The rows' scales go into the scores and into P, which bf16
+//     holds without loss, and P carries 2^100 so that nothing underflows.
 #include "kv_cache.cuh"
 #include "sm100.cuh"
+#include "tma_map.cuh"
 
 namespace bsa {
 namespace {
@@ -31,32 +32,36 @@ using namespace kv;
 using sm100::ex2_approx;
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = kWarps * 32 + 32;           // and the producer's warp
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLift = 100.f;                       // e4m3: P carries 2^100 ...
+constexpr float kBack = 0x1p120f;                    // ... as does l, and V's operand is 2^-120 V
 
 template <bool FP8, int M>
 struct Cfg {
-    static constexpr int kStepBytes = FP8 ? 2048 + 512 : 4096;   // 16 keys of K and V (and scales)
-    static constexpr int kStages = FP8 ? (M == 8 ? 4 : 4) : (M == 8 ? 3 : 2);
-    static constexpr size_t kRing = (size_t)kWarps * kStages * kStepBytes;
-    static constexpr size_t kMerge = (size_t)kWarps * M * 66 * 4;
-    static constexpr size_t kSmem = kRing + kMerge;
+    // e4m3: K, V, and their scales; bf16: K and V. Two blocks share an SM.
+    static constexpr uint32_t kV = FP8 ? 8192 : 16384;
+    static constexpr uint32_t kStage = FP8 ? 2 * 8192 + 2 * 128 : 2 * 16384;
+    static constexpr int NS = FP8 ? (M == 8 ? 5 : 4) : (M == 8 ? 3 : 2);
+    static constexpr uint32_t kMerge = NS * kStage;                   // [warp][row][64 + 2]
+    static constexpr uint32_t kCtl = kMerge + kWarps * M * 66 * 4;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+template <int M>
+struct Ctl {
+    uint64_t full[5], empty[5];
+    uint64_t rec_full[2], rec_empty[2], meet;
+    Rec rec[2];
+    int meta[5], tile[5];
+    uint32_t poison[M][2];                  // columns of a row that met a NaN or infinite value
+    int abort;
+    Start start;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort, status));
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
@@ -66,11 +71,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 
@@ -96,13 +96,12 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
-// f16 with at most 7 mantissa bits to the bf16 2^-112 times as large: the exponent fields, 15 and
-// 127 off, are not converted
-__device__ __forceinline__ uint32_t bf16_of(uint32_t h) {
-    return ((h >> 3) & 0x0fff0fffu) | (h & 0x80008000u);
+// byte j of two words of codes to the bf16 pair 2^-120 times their values: sign, then the 7 bits
+// of exponent and mantissa moved into a bf16's (subnormal codes become subnormal bf16)
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t a, uint32_t b, int j) {
+    const uint32_t y = __byte_perm(a, b, j | j << 4 | (4 + j) << 8 | (4 + j) << 12);
+    return ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
 }
-constexpr uint32_t kVExp = 100;             // P carries 2^100 ...
-constexpr float kVBack = 4096.f;            // ... and O 2^(112 - 100) in the end
 
 __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -110,118 +109,127 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
 
 template <bool FP8, int M>
 __global__ void __launch_bounds__(kThreads, 2)
-kv_rows_kernel(const AttnArgs a) {
+kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+    using namespace sm100;
     using C = Cfg<FP8, M>;
     constexpr int NH = M / 8;               // 8-row halves in use
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Start start;
-    __shared__ uint32_t poison[M][2];       // columns of a row that met a NaN or infinite value
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctl<M>& ctl = *reinterpret_cast<Ctl<M>*>(smem + C::kCtl);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
     const int team = blockIdx.x;
+    volatile int* abort = &ctl.abort;
 
-    if (tid < M * 2) (&poison[0][0])[tid] = 0u;
+    if (tid == 0) {
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], kWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl.rec_full[s], 1);
+            mbar_init(&ctl.rec_empty[s], kWarps);
+        }
+        mbar_init(&ctl.meet, kWarps);
+        ctl.abort = 0;
+        fence_mbar_init();
+    }
+    if (tid < M * 2) (&ctl.poison[0][0])[tid] = 0u;
     let_next_start();
     wait_for_previous();
+    // tile swizzles assume a 1024-byte aligned base; refuse to run otherwise
+    if ((smem_u32(smem) & 1023u) != 0u) {
+        if (tid == 0) {
+            record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
+            a.desc[team * kDesc] = 0;
+        }
+        return;
+    }
     int* tables = reinterpret_cast<int*>(smem);
-    const Start st = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &start);
+    const Start st = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &ctl.start);
     if (tid == 0) a.desc[team * kDesc] = 0;
     if (team >= st.teams || st.total == 0) return;
+    fence_async_shared();                   // the plan's tables lay where TMA writes next
     __syncthreads();
 
-    const uint32_t ring = sm100::smem_u32(smem) + warp * (C::kStages * C::kStepBytes);
-    float* mo = reinterpret_cast<float*>(smem + C::kRing);            // [warp][row][64]
-    float* mml = mo + kWarps * M * 64;                                // [warp][row][2]
-
-    // the loader runs kStages - 1 steps ahead of the arithmetic, across items; lane i holds the
-    // page of the unit lbase + i of the loader's segment
-    Walk lw(a, st, team);
-    bool live = lw.next();
-    int lj = live ? lw.j0 : 0, lbase = lj - 32, lpage = -1;
-    uint32_t held = 0u;                     // bit s: stage s holds keys
-    auto load_step = [&](int stage) {
-        bool ok = false;
-        if (live) {
-            if (lj - lbase >= 32) {
-                lbase = lj;
-                lpage = -1;
-                const int k = unit_of(lw.span, lj + lane) * kUnit + warp * 16;
-                if (lj + lane < lw.j1 && k < lw.span.hi_max && (k + 16 > lw.span.lo_min || k < a.sink))
-                    lpage = a.c.table[(long long)lw.s * a.c.max_pages + (k >> a.c.pshift)];
-                if (lpage >= a.c.pages) {
-                    record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
-                    lpage = -1;
+    if (warp == kWarps) {
+        // ============================================================ producer
+        int U = 0, X = 0;
+        auto put_record = [&](const Rec& r) -> bool {
+            const int slot = X & 1;
+            if (X >= 2 && !warp_wait(&ctl.rec_empty[slot], ((X >> 1) - 1) & 1, abort, a.status)) return false;
+            if (lane == 0) {
+                ctl.rec[slot] = r;
+                mbar_arrive(&ctl.rec_full[slot]);
+            }
+            ++X;
+            return true;
+        };
+        auto begin = [](const Walk&, int) { return true; };
+        auto put_tile = [&](int meta, int t, int page, long long row, unsigned have, int at, int box) -> bool {
+            const int s = U % C::NS;
+            if (U >= C::NS && !warp_wait(&ctl.empty[s], ((U / C::NS) - 1) & 1, abort, a.status)) return false;
+            uint8_t* dst = smem + s * C::kStage;
+            if (lane == 0) {
+                ctl.meta[s] = meta;
+                ctl.tile[s] = t;
+                mbar_arrive_expect_tx(&ctl.full[s], __popc(have) * box * (FP8 ? 130 : 256));
+            }
+            __syncwarp();
+            if (page >= 0) {
+                if (FP8) {
+                    bulk_load(dst + at * 64, static_cast<const uint8_t*>(a.k) + row * 64, box * 64, &ctl.full[s]);
+                    bulk_load(dst + C::kV + at * 64, static_cast<const uint8_t*>(a.v) + row * 64, box * 64, &ctl.full[s]);
+                    bulk_load(dst + 16384 + at, a.ks + row, box, &ctl.full[s]);
+                    bulk_load(dst + 16384 + 128 + at, a.vs + row, box, &ctl.full[s]);
+                } else {
+                    tma_load_2d(dst + at * 128, &tm_k, &ctl.full[s], 0, (int)row);
+                    tma_load_2d(dst + C::kV + at * 128, &tm_v, &ctl.full[s], 0, (int)row);
                 }
             }
-            const int page = __shfl_sync(0xffffffffu, lpage, lj - lbase);
-            ok = page >= 0;
-            {
-                const int kb = unit_of(lw.span, lj) * kUnit + warp * 16;
-                if (ok) {
-                    const long long row =
-                        (((long long)page * a.c.kv_heads + lw.h) << a.c.pshift) + (kb & ((1 << a.c.pshift) - 1));
-                    const uint32_t dst = ring + stage * C::kStepBytes;
-                    if (!FP8) {
-                        const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * 128;
-                        const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * 128;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                cp16(dst + (j * 2 + c) * 512 + lane * 16, kp + (j * 8 + g) * 128 + c * 64 + t * 16);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            cp16(dst + 2048 + i * 512 + lane * 16, vp + (2 * t + (i & 1) + (i >> 1) * 8) * 128 + g * 16);
-                    } else {
-                        const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * 64;
-                        const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * 64;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            cp16(dst + j * 512 + lane * 16, kp + (j * 8 + g) * 64 + t * 16);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            cp8(dst + 1024 + i * 256 + lane * 8, vp + (2 * t + (i & 1) + (i >> 1) * 8) * 64 + g * 8);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            cp4(dst + 2048 + i * 128 + lane * 4, a.ks + row + i * 8 + (t >> 1) * 4);
-                            cp4(dst + 2304 + i * 128 + lane * 4, a.vs + row + i * 8 + (t >> 1) * 4);
-                        }
-                    }
-                }
-            }
-            if (++lj >= lw.j1) {
-                lw.done();
-                live = lw.next();
-                lj = live ? lw.j0 : 0;
-                lbase = lj - 32;
-            }
+            ++U;
+            return true;
+        };
+        if (produce(a, st, team, 0, lane, put_record, begin, put_tile)) {
+            Rec rec = {};
+            rec.tiles = -1;
+            put_record(rec);
         }
-        held = (held & ~(1u << stage)) | ((ok ? 1u : 0u) << stage);
-        cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) load_step(i);
+        // every copy has landed before the block's shared memory goes away
+        volatile int never = 0;
+        for (int u = max(0, U - C::NS); u < U; ++u)
+            mbar_wait(&ctl.full[u % C::NS], (u / C::NS) & 1, &never, a.status, 50000000ull);
+        return;
+    }
 
-    Walk w(a, st, team);
-    int stage = 0;
-    while (w.next()) {
-        const Seq q = w.q;
-        const int nrows = q.n * a.group;
-        const int r0 = w.rg * M;            // R = 1, mr = M: a row group is one query tile
+    // ================================================================ arithmetic
+    float* mo = reinterpret_cast<float*>(smem + C::kMerge);           // [warp][row][64]
+    float* mml = mo + kWarps * M * 64;                                // [warp][row][2]
+    const int g = lane >> 2, t = lane & 3;
+    int U = 0, met = 0;
+    auto meet = [&]() -> bool {             // the eight warps; bounded like every wait
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.meet);
+        return warp_wait(&ctl.meet, met++ & 1, abort, a.status);
+    };
+    for (int X = 0;; ++X) {
+        if (!warp_wait(&ctl.rec_full[X & 1], (X >> 1) & 1, abort, a.status)) break;
+        const Rec& rec = ctl.rec[X & 1];
+        const int tiles = rec.tiles;
+        if (tiles < 0) break;
+        const int nrows = rec.nrows, r0 = rec.r0, row0 = rec.row0, pos0 = rec.pos0, len = rec.len;
         // ---------------------------------------------------------------- Q
         uint32_t qf[4][2 * NH];
         float rowf[NH];                     // x = score * rowf
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
-            const int r = r0 + hh * 8 + g;
+            const int r = hh * 8 + g;
             uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
             if (r < nrows) {
-                const int i = r / a.group;
+                const int i = (r0 + r) / a.group;
                 const __nv_bfloat16* p =
-                    a.q + (long long)(q.row0 + i) * a.q_stride + ((long long)w.h * a.group + (r - i * a.group)) * 64;
+                    a.q + (long long)(row0 + i) * a.q_stride + ((long long)rec.h * a.group + (r0 + r - i * a.group)) * 64;
                 const uint4* p4 = reinterpret_cast<const uint4*>(p);
-                c0 = p4[FP8 ? 2 * t : t];
-                c1 = p4[FP8 ? 2 * t + 1 : 4 + t];
+                c0 = p4[2 * t];
+                c1 = p4[2 * t + 1];
             }
             uint32_t wds[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
             rowf[hh] = kScaleLog2;
@@ -251,6 +259,7 @@ kv_rows_kernel(const AttnArgs a) {
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+        constexpr float kUp = FP8 ? kLift : 0.f;   // m is kUp below the largest score (log2 units)
         float m[NH], l[NH];
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
@@ -258,31 +267,42 @@ kv_rows_kernel(const AttnArgs a) {
             l[hh] = 0.f;
         }
 
-        for (int j = w.j0; j < w.j1; ++j) {
-            cp_wait<C::kStages - 2>();
-            const bool ok = (held >> stage) & 1u;
-            const uint32_t src = ring + stage * C::kStepBytes;
-            const int kb = unit_of(w.span, j) * kUnit + warp * 16;
-            // the stage that the previous step emptied
-            load_step(stage == 0 ? C::kStages - 1 : stage - 1);
-            stage = stage + 1 == C::kStages ? 0 : stage + 1;
-            if (!ok) continue;
+        for (int u = 0; u < tiles; ++u, ++U) {
+            const int s = U % C::NS;
+            if (!warp_wait(&ctl.full[s], (U / C::NS) & 1, abort, a.status)) return;
+            const int meta = ctl.meta[s], kb = ctl.tile[s] * kUnit + warp * 16;
+            const bool want = ((meta >> warp) & 1) &&
+                              ((meta & kFull) || (kb < rec.hi_max && (kb + 16 > rec.lo_min || kb < a.sink)));
+            const bool all = (meta & kFull) || (kb + 16 <= rec.hi_min &&
+                                                (kb >= rec.lo_max || kb + 16 <= min(a.sink, rec.lo_min)));
+            if (!want) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.empty[s]);
+                continue;
+            }
+            // key of the warp's 16 that column x (0 .. 7) of the scores' half jj stands for
+            auto key_of = [](int jj, int x) {
+                return FP8 ? jj * 8 + (x & 1 ? 4 + ((x >> 1) ^ 1) : x >> 1) : jj * 8 + x;
+            };
+            const uint32_t src = smem_u32(smem + s * C::kStage);
             // ------------------------------------------------------------ scores
             float x[2][4];
+            float ksc[2][2], vsc[2][2];
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) x[jj][c] = 0.f;
+                const int r = warp * 16 + key_of(jj, g);
                 if (!FP8) {
-                    const uint4 k0 = lds16(src + (jj * 2) * 512 + lane * 16);
-                    const uint4 k1 = lds16(src + (jj * 2 + 1) * 512 + lane * 16);
+                    const uint4 k0 = lds16(src + r * 128 + (((2 * t) ^ (r & 7)) << 4));
+                    const uint4 k1 = lds16(src + r * 128 + (((2 * t + 1) ^ (r & 7)) << 4));
                     const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16(x[jj], qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
                                  kw[2 * ks], kw[2 * ks + 1]);
                 } else {
-                    const uint4 k0 = lds16(src + jj * 512 + lane * 16);
+                    const uint4 k0 = lds16(src + r * 64 + t * 16);
                     const uint32_t kw[4] = {k0.x, k0.y, k0.z, k0.w};
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
@@ -290,21 +310,23 @@ kv_rows_kernel(const AttnArgs a) {
                                 half2_of(kw[ks], false), half2_of(kw[ks], true));
                 }
             }
-            float vsc[2][2];
             if (FP8) {
+                // scale bytes of the warp's keys: those of a lane's columns are bytes t, 4 + (t ^ 1) of
+                // each half. 255 << 23 is infinite, and inf - inf makes the score NaN.
+                const uint4 kb4 = lds16(src + 16384 + warp * 16), vb4 = lds16(src + 16384 + 128 + warp * 16);
+                const uint32_t kw[4] = {kb4.x, kb4.y, kb4.z, kb4.w}, vw[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const uint32_t kw = lds4(src + 2048 + jj * 128 + lane * 4) >> ((t & 1) * 16);
-                    const uint32_t vw = lds4(src + 2304 + jj * 128 + lane * 4) >> ((t & 1) * 16);
+                for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float kf = scale_of((kw >> (8 * c)) & 255u);
-                        const uint32_t vb = (vw >> (8 * c)) & 255u;
-                        vsc[jj][c] = vb >= 155u ? __uint_as_float(0x7fc00000u) : pow2_of(vb + kVExp);
+                        const int at = c ? t ^ 1 : t;
+                        ksc[jj][c] = __uint_as_float(((kw[2 * jj + c] >> (8 * at)) << 23) & 0x7f800000u);
+                        vsc[jj][c] = __uint_as_float(((vw[2 * jj + c] >> (8 * at)) << 23) & 0x7f800000u);
+                        const float zero = ksc[jj][c] - ksc[jj][c];
 #pragma unroll
-                        for (int hh = 0; hh < NH; ++hh) x[jj][2 * hh + c] *= kf * rowf[hh];
+                        for (int hh = 0; hh < NH; ++hh)
+                            x[jj][2 * hh + c] = fmaf(x[jj][2 * hh + c], ksc[jj][c] * rowf[hh], zero);
                     }
-                }
             } else {
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj)
@@ -312,45 +334,46 @@ kv_rows_kernel(const AttnArgs a) {
                     for (int c = 0; c < 2 * NH; ++c) x[jj][c] *= kScaleLog2;
             }
             // ------------------------------------------------------------ V, and what is seen
-            uint32_t vw[4][4];              // key i of the lane's four: 8 values (bf16) or codes
+            uint32_t vw[4][4];              // keys of the lane's four columns: 8 values (bf16) or codes
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const int r = warp * 16 + key_of(i >> 1, 2 * t + (i & 1));
                 if (!FP8) {
-                    const uint4 v = lds16(src + 2048 + i * 512 + lane * 16);
+                    const uint4 v = lds16(src + C::kV + r * 128 + ((g ^ (r & 7)) << 4));
                     vw[i][0] = v.x;
                     vw[i][1] = v.y;
                     vw[i][2] = v.z;
                     vw[i][3] = v.w;
                 } else {
-                    const uint2 v = lds8(src + 1024 + i * 256 + lane * 8);
+                    const uint2 v = lds8(src + C::kV + r * 64 + g * 8);
                     vw[i][0] = v.x;
                     vw[i][1] = v.y;
                 }
             }
-            const Span& sp = w.span;
-            const bool all = kb + 16 <= sp.hi_min && (kb >= sp.lo_max || kb + 16 <= min(a.sink, sp.lo_min));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.empty[s]);
             uint32_t seen = 0xffu;          // bit (jj * 4 + c): x[jj][c] counts
             if (!all) {
                 seen = 0u;
 #pragma unroll
                 for (int hh = 0; hh < NH; ++hh) {
-                    const int r = r0 + hh * 8 + g;
+                    const int r = hh * 8 + g;
                     int lo = 0, hi = 0;
-                    if (r < nrows) visible(a, q.len, q.len - q.n + r / a.group, lo, hi);
+                    if (r < nrows) visible(a, len, pos0 + (r0 + r) / a.group, lo, hi);
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const int key = kb + jj * 8 + 2 * t + c;
+                            const int key = kb + key_of(jj, 2 * t + c);
                             if (key < hi && (key >= lo || key < a.sink)) seen |= 1u << (jj * 4 + 2 * hh + c);
                         }
                 }
                 if (!FP8) {
-                    // P = 0 does not silence a NaN: rows of V past the end are dropped, and a
-                    // non-finite value that only some rows see is kept apart
+                    // P = 0 does not silence a NaN: non-finite values are taken out of V and marked
+                    // in the rows that see them (none, past the end)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int key = kb + 2 * t + (i & 1) + (i >> 1) * 8;
+                        const int key = kb + key_of(i >> 1, 2 * t + (i & 1));
                         bool bad = false;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) bad |= has_nonfinite(vw[i][k]);
@@ -367,11 +390,11 @@ kv_rows_kernel(const AttnArgs a) {
                                     vw[i][k] &= 0xffffu;
                                 }
                             }
-                            for (int r = r0; r < min(r0 + M, nrows); ++r) {
+                            for (int r = 0; r < nrows; ++r) {
                                 int lo, hi;
-                                visible(a, q.len, q.len - q.n + r / a.group, lo, hi);
+                                visible(a, len, pos0 + (r0 + r) / a.group, lo, hi);
                                 if (key < hi && (key >= lo || key < a.sink))
-                                    atomicOr(&poison[r - r0][g >> 2], cols << ((g & 3) * 8));
+                                    atomicOr(&ctl.poison[r][g >> 2], cols << ((g & 3) * 8));
                             }
                         }
                     }
@@ -388,7 +411,7 @@ kv_rows_kernel(const AttnArgs a) {
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {
                 top[hh] = fmaxf(fmaxf(x[0][2 * hh], x[0][2 * hh + 1]), fmaxf(x[1][2 * hh], x[1][2 * hh + 1]));
-                need |= top[hh] > m[hh] + kRescale;
+                need |= top[hh] > m[hh] + (kRescale + kUp);
             }
             if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -396,7 +419,7 @@ kv_rows_kernel(const AttnArgs a) {
                     float n = top[hh];
                     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
                     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
-                    n = fmaxf(n, m[hh]);
+                    n = fmaxf(n - kUp, m[hh]);
                     const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
                     m[hh] = n;
                     l[hh] *= f;
@@ -437,17 +460,9 @@ kv_rows_kernel(const AttnArgs a) {
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t sel = z ? 0x7362u : 0x5140u;
-                        const uint32_t ab = __byte_perm(vw[0][k], vw[1][k], sel);
-                        const uint32_t cd = __byte_perm(vw[2][k], vw[3][k], sel);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            mma_bf16(o[4 * k + 2 * z + y], pf[0][0], p1a, pf[1][0], p1b, bf16_of(half2_of(ab, y)),
-                                     bf16_of(half2_of(cd, y)));
-                    }
+                for (int j8 = 0; j8 < 8; ++j8)
+                    mma_bf16(o[j8], pf[0][0], p1a, pf[1][0], p1b, bf16_pair(vw[0][j8 >> 2], vw[1][j8 >> 2], j8 & 3),
+                             bf16_pair(vw[2][j8 >> 2], vw[3][j8 >> 2], j8 & 3));
             }
         }
 
@@ -469,9 +484,9 @@ kv_rows_kernel(const AttnArgs a) {
                 mml[r * 2 + 1] = l[hh];
             }
         }
-        __syncthreads();
-        const bool whole = w.has_start && w.has_end;
-        float* part = part_at<M>(a, team, w.has_start ? 1 : 0, 0);
+        if (!meet()) return;
+        const bool whole = rec.whole;
+        float* part = part_at<M>(a, team, rec.run, 0);
         if (tid < M * 16) {
             const int r = tid >> 4, c4 = (tid & 15) * 4;
             float mm = -INFINITY, ll = 0.f;
@@ -490,41 +505,31 @@ kv_rows_kernel(const AttnArgs a) {
                 acc[3] += f * v.w;
             }
             // l = 0: nothing seen. NaN stays.
-            const float inv = (ll == 0.f ? 0.f : 1.f / ll) * (FP8 ? kVBack : 1.f);
-            const uint32_t bad = poison[r][c4 >> 5] >> (c4 & 31);
+            const float inv = (ll == 0.f ? 0.f : 1.f / ll) * (FP8 ? kBack : 1.f);
+            const uint32_t bad = ctl.poison[r][c4 >> 5] >> (c4 & 31);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 acc[k] *= inv;
                 if ((bad >> k) & 1u) acc[k] = __uint_as_float(0x7fc00000u);
             }
             const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-            if (r0 + r < nrows) {
+            if (r < nrows) {
                 if (whole) {
                     const int i = (r0 + r) / a.group;
-                    const int head = w.h * a.group + (r0 + r - i * a.group);
-                    *reinterpret_cast<uint2*>(a.out + (long long)(q.row0 + i) * a.out_stride + head * 64 + c4) =
+                    const int head = rec.h * a.group + (r0 + r - i * a.group);
+                    *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + c4) =
                         make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
-                    if (c4 == 0 && a.lse != nullptr) a.lse[(long long)head * a.rows + q.row0 + i] = lse;
+                    if (c4 == 0 && a.lse != nullptr) a.lse[(long long)head * a.rows + row0 + i] = lse;
                 } else {
                     *reinterpret_cast<float4*>(part + r * 64 + c4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (c4 == 0) part[M * 64 + r] = lse;
                 }
             }
         }
-        if (tid == 0 && !whole && w.has_start) {   // the merge kernel's record of this item
-            int* d = a.desc + team * kDesc;
-            d[1] = q.row0;
-            d[2] = q.n;
-            d[3] = w.h;
-            d[4] = w.rg;
-            d[5] = st.team_of(w.item + max(1, w.span.count) - 1);
-            d[0] = 1;
-        }
-        __syncthreads();
-        if (tid < M * 2) (&poison[0][0])[tid] = 0u;
-        w.done();
+        if (!meet()) return;
+        if (tid < M * 2) (&ctl.poison[0][0])[tid] = 0u;
+        if (lane == 0) mbar_arrive(&ctl.rec_empty[X & 1]);
     }
-    cp_wait<0>();
 }
 
 // Joins the partial results of an item that crosses team ends: the team that holds its first
@@ -608,9 +613,15 @@ template <bool FP8, int M>
 cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
     using C = Cfg<FP8, M>;
     auto kern = kv_rows_kernel<FP8, M>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    const size_t smem = C::kCtl + sizeof(Ctl<M>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_early(kern, dim3(a.max_teams), kThreads, C::kSmem, st, a);
+    CUtensorMap k = {}, v = {};
+    const uint64_t rows = ((uint64_t)a.c.pages * a.c.kv_heads) << a.c.pshift;
+    const uint32_t box = a.c.pshift < 7 ? 1u << a.c.pshift : 128u;
+    if (!FP8 && (!make_tile_map(&k, a.k, rows, 64, box, false) || !make_tile_map(&v, a.v, rows, 64, box, false)))
+        return cudaErrorInvalidValue;
+    return launch_early(kern, dim3(a.max_teams), kThreads, smem, st, k, v, a);
 }
 
 }  // namespace

@@ -52,27 +52,16 @@ struct Cfg {
     static constexpr uint32_t kOffCtl = kOffRaw + (FP8 ? kRaw * kRawHalf : 0);
 };
 
-// What the softmax has to know of a segment.
-struct Rec {
-    int tiles;             // key tiles to come (0: nothing to see); negative: no further segment
-    int nrows, r0;         // rows of the query tile, first one within the chunk
-    int row0, pos0, len;   // packed row and position of the chunk's first token, cached tokens
-    int h, whole, run;     // key/value head; the segment is the whole item; run of the partial result
-    int lo_min, hi_max;    // positions outside the sink that some row sees
-};
-
-// Per key tile: page mask (a bit per 16 keys) and these.
-enum { kFull = 0x100, kFirst = 0x200, kLast = 0x400, kEnd = 0x800 };
-
 struct Ctl {
     uint64_t q_full, q_empty;
     uint64_t k_full[3], kv_empty[3], v_full[3];      // v_full: e4m3 only (bf16: with k_full)
     uint64_t raw_full[kRaw], raw_empty[kRaw];
-    uint64_t rec_full[2], rec_empty[2];
+    uint64_t rec_full[2], rec_empty[2], meet;
     uint64_t s_full, s_free, p_full, o_done, o_final, drain;
     Rec rec[2];
     int meta[3], tile[3];                            // of the stages
     int raw_meta[kRaw], raw_tile[kRaw];
+    int found;                                       // the last tile (count) with values taken out
     uint32_t tmem_base;
     int abort;
     Start start;
@@ -147,6 +136,8 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&ctl.o_done, 1);
         mbar_init(&ctl.o_final, 1);
         mbar_init(&ctl.drain, 1);
+        mbar_init(&ctl.meet, 4);
+        ctl.found = 0;
         ctl.abort = 0;
         fence_mbar_init();
     }
@@ -172,10 +163,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
             // ======================================================== producer
-            const int box = min(1 << a.c.pshift, 128), shift = min(a.c.pshift, 7);   // keys of a TMA box
             int U = 0, I = 0, X = 0;     // tiles, Q tiles, segments so far
-            bool ok = true;
-            Walk w(a, start, team);
             auto put_record = [&](const Rec& r) -> bool {
                 const int slot = X & 1;
                 if (X >= 2 && !warp_wait(&ctl.rec_empty[slot], ((X >> 1) - 1) & 1, abort, a.status)) return false;
@@ -186,126 +174,57 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 ++X;
                 return true;
             };
-            while (ok && w.next()) {
-                const int r0 = (w.rg * a.R + member) * a.mr;
-                const int nrows = min(a.mr, w.q.n * a.group - r0);
-                if (nrows <= 0) {
-                    w.done();
-                    continue;
+            auto begin = [&](const Walk& w, int r0) -> bool {
+                if (I > 0 && !warp_wait(&ctl.q_empty, (I - 1) & 1, abort, a.status)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&ctl.q_full, a.mr * 128);
+                    tma_load_3d(smem + C::kOffQ, &tm_q, &ctl.q_full, 0, w.h * a.group, w.q.row0 + r0 / a.group);
                 }
-                const Span own = rows_span(a, w.q, r0, r0 + a.mr);
-                auto wanted = [&](int k0, int n) { return k0 < own.hi_max && (k0 + n > own.lo_min || k0 < a.sink); };
-                // how many of the run's tiles this query tile needs: of the tiles [0, sinks) and
-                // [lo, hi) those that the run's two stretches (unit_of) hold
-                const int hi = (own.hi_max + kUnit - 1) / kUnit, lo = own.lo_min / kUnit;
-                const int sinks = min(min((int)(((long long)a.sink + kUnit - 1) / kUnit), lo), hi);
-                auto held = [&](int p, int q) {
-                    return max(0, min(q, sinks) - p) + max(0, min(q, hi) - max(p, lo));
-                };
-                const int skip = w.span.t_lo - w.span.n_sink;
-                const int tiles = held(w.j0, min(w.j1, w.span.n_sink)) + held(max(w.j0, w.span.n_sink) + skip, w.j1 + skip);
-                Rec rec;
-                rec.tiles = tiles;
-                rec.nrows = nrows;
-                rec.r0 = r0;
-                rec.row0 = w.q.row0;
-                rec.pos0 = w.q.len - w.q.n;
-                rec.len = w.q.len;
-                rec.h = w.h;
-                rec.whole = w.has_start && w.has_end;
-                rec.run = w.has_start ? 1 : 0;
-                rec.lo_min = own.lo_min;
-                rec.hi_max = own.hi_max;
-                if (!put_record(rec)) break;
-                if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
-                    int* d = a.desc + team * kDesc;
-                    d[1] = w.q.row0;
-                    d[2] = w.q.n;
-                    d[3] = w.h;
-                    d[4] = w.rg;
-                    d[5] = start.team_of(w.item + max(1, w.span.count) - 1);
-                    d[0] = 1;
-                }
-                if (tiles > 0) {
-                    if (I > 0 && !warp_wait(&ctl.q_empty, (I - 1) & 1, abort, a.status)) break;
+                q_loads = ++I;
+                return true;
+            };
+            auto put_tile = [&](int meta, int t, int page, long long row, unsigned have, int at, int box) -> bool {
+                if (!FP8) {
+                    const int st = U % NS;
+                    if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) return false;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&ctl.q_full, a.mr * 128);
-                        tma_load_3d(smem + C::kOffQ, &tm_q, &ctl.q_full, 0, w.h * a.group, w.q.row0 + r0 / a.group);
+                        ctl.meta[st] = meta;
+                        ctl.tile[st] = t;
+                        mbar_arrive_expect_tx(&ctl.k_full[st], __popc(have) * box * 256);
                     }
-                    q_loads = ++I;
-                }
-                int left = tiles;
-                for (int j = w.j0; left > 0 && j < w.j1; ++j) {
-                    const int t = unit_of(w.span, j);
-                    if (!wanted(t * kUnit, kUnit)) continue;
-                    // the pages of the tile, one box per lane
-                    const int k0 = t * kUnit + lane * box;
-                    int page = -1;
-                    if (lane < (128 >> shift) && wanted(k0, box))
-                        page = a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)];
-                    if (page >= a.c.pages) {
-                        record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
-                        page = -1;
+                    __syncwarp();
+                    if (page >= 0) {
+                        tma_load_2d(smem + C::kOffK + st * kTile + at * 128, &tm_k, &ctl.k_full[st], 0, (int)row);
+                        tma_load_2d(smem + C::kOffV + st * kTile + at * 128, &tm_v, &ctl.k_full[st], 0, (int)row);
                     }
-                    const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
-                    int meta = (left == tiles ? kFirst : 0) | (left == 1 ? kLast : 0);
-                    --left;
+                    issued = U + 1;
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) meta |= ((have >> ((i * 16) >> shift)) & 1u) << i;
-                    const int key = t * kUnit;
-                    if ((meta & 0xff) == 0xff && key + kUnit <= own.hi_min &&
-                        (key >= own.lo_max || key + kUnit <= min(a.sink, own.lo_min)))
-                        meta |= kFull;
-                    const long long row = page < 0 ? 0
-                        : (((long long)page * a.c.kv_heads + w.h) << a.c.pshift) + (k0 & ((1 << a.c.pshift) - 1));
-                    const uint32_t at = lane * box;
-                    if (!FP8) {
-                        const int st = U % NS;
-                        if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) {
-                            ok = false;
-                            break;
-                        }
+                    for (int half = 0; half < 2; ++half) {
+                        const int x = 2 * U + half, slot = x % kRaw;
+                        if (x >= kRaw && !warp_wait(&ctl.raw_empty[slot], ((x / kRaw) - 1) & 1, abort, a.status))
+                            return false;
+                        uint8_t* dst = smem + C::kOffRaw + slot * kRawHalf;
                         if (lane == 0) {
-                            ctl.meta[st] = meta;
-                            ctl.tile[st] = t;
-                            mbar_arrive_expect_tx(&ctl.k_full[st], __popc(have) * box * 256);
+                            ctl.raw_meta[slot] = meta;
+                            ctl.raw_tile[slot] = t;
+                            mbar_arrive_expect_tx(&ctl.raw_full[slot], __popc(have) * box * 65);
                         }
                         __syncwarp();
                         if (page >= 0) {
-                            tma_load_2d(smem + C::kOffK + st * kTile + at * 128, &tm_k, &ctl.k_full[st], 0, (int)row);
-                            tma_load_2d(smem + C::kOffV + st * kTile + at * 128, &tm_v, &ctl.k_full[st], 0, (int)row);
+                            bulk_load(dst + at * 64, static_cast<const uint8_t*>(half ? a.v : a.k) + row * 64, box * 64,
+                                      &ctl.raw_full[slot]);
+                            bulk_load(dst + 8192 + at, (half ? a.vs : a.ks) + row, box, &ctl.raw_full[slot]);
                         }
-                        issued = U + 1;
-                    } else {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int x = 2 * U + half, slot = x % kRaw;
-                            if (x >= kRaw && !warp_wait(&ctl.raw_empty[slot], ((x / kRaw) - 1) & 1, abort, a.status)) {
-                                ok = false;
-                                break;
-                            }
-                            uint8_t* dst = smem + C::kOffRaw + slot * kRawHalf;
-                            if (lane == 0) {
-                                ctl.raw_meta[slot] = meta;
-                                ctl.raw_tile[slot] = t;
-                                mbar_arrive_expect_tx(&ctl.raw_full[slot], __popc(have) * box * 65);
-                            }
-                            __syncwarp();
-                            if (page >= 0) {
-                                bulk_load(dst + at * 64, static_cast<const uint8_t*>(half ? a.v : a.k) + row * 64, box * 64,
-                                          &ctl.raw_full[slot]);
-                                bulk_load(dst + 8192 + at, (half ? a.vs : a.ks) + row, box, &ctl.raw_full[slot]);
-                            }
-                            issued = x + 1;
-                        }
-                        if (!ok) break;
+                        issued = x + 1;
                     }
-                    ++U;
                 }
-                w.done();
-            }
+                ++U;
+                return true;
+            };
+            const bool ok = produce(a, start, team, member, lane, put_record, begin, put_tile);
             // no further tile, no further segment
-            if (ok && !*abort) {
+            if (ok) {
                 const int st = U % NS, x = 2 * U, slot = x % kRaw;
                 if (!FP8 ? U < NS || warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)
                          : x < kRaw || warp_wait(&ctl.raw_empty[slot], ((x / kRaw) - 1) & 1, abort, a.status)) {
@@ -440,7 +359,12 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        int U = 0, I = 0;
+        int U = 0, I = 0, met = 0;
+        auto meet = [&]() -> bool {   // the four warps; bounded like every wait
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.meet);
+            return warp_wait(&ctl.meet, met++ & 1, abort, a.status);
+        };
         for (int X = 0;; ++X) {
             if (!warp_wait(&ctl.rec_full[X & 1], (X >> 1) & 1, abort, a.status)) break;
             const Rec& rec = ctl.rec[X & 1];
@@ -520,15 +444,12 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     // rare: K's tile is done with (S is read), so its memory passes the columns on
-                    uint32_t found;
-                    asm volatile(
-                        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                        : "=r"(found) : "r"(bad0 | bad1) : "memory");
-                    if (found) {
+                    if (bad0 | bad1) ctl.found = U + 1;
+                    if (!meet()) { ok = false; break; }
+                    if (*(volatile int*)&ctl.found == U + 1) {
                         uint2* list = reinterpret_cast<uint2*>(smem + C::kOffK + st * kTile);
                         list[row] = make_uint2(bad0, bad1);
-                        asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+                        if (!meet()) { ok = false; break; }
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k)
 #pragma unroll 1
@@ -538,7 +459,6 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                     poison0 |= b.x;
                                     poison1 |= b.y;
                                 }
-                        asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
                     }
                     fence_async_shared();
                 }

@@ -347,6 +347,95 @@ struct Walk {
     }
 };
 
+// What the arithmetic of a block has to know of a segment.
+struct Rec {
+    int tiles;             // key tiles to come (0: nothing to see); negative: no further segment
+    int nrows, r0;         // rows of the query tile, first one within the chunk
+    int row0, pos0, len;   // packed row and position of the chunk's first token, cached tokens
+    int h, whole, run;     // key/value head; the segment is the whole item; run of the partial result
+    int lo_min, hi_max;    // positions outside the sink that some row sees
+    int lo_max, hi_min;    // [lo_max, hi_min) is seen by every row
+};
+
+// Words of a key tile: a bit per 16 keys whose page exists, and these.
+enum { kFull = 0x100, kFirst = 0x200, kLast = 0x400, kEnd = 0x800 };
+
+// The producer's part of a block, run by one warp: walks the team's segments, hands out a record
+// for each (put_record), announces those with key tiles (begin) and then hands out their tiles
+// (put_tile), one box of up to 128 keys of a page per lane: `page` (negative: none), `row`, its
+// first row in the pools, `at`, the box's first key within the tile, and the lanes that have one. Any of
+// the three returns false to stop. True when all is handed out.
+template <class PutRecord, class Begin, class PutTile>
+__device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, int team, int member, int lane,
+                                        PutRecord put_record, Begin begin, PutTile put_tile) {
+    const int box = min(1 << a.c.pshift, kUnit), shift = min(a.c.pshift, 7);
+    Walk w(a, start, team);
+    for (; w.next(); w.done()) {
+        const int r0 = (w.rg * a.R + member) * a.mr;
+        const int nrows = min(a.mr, w.q.n * a.group - r0);
+        if (nrows <= 0) continue;
+        const Span own = rows_span(a, w.q, r0, r0 + a.mr);
+        auto wanted = [&](int k0, int n) { return k0 < own.hi_max && (k0 + n > own.lo_min || k0 < a.sink); };
+        // how many of the run's tiles this query tile needs: of the tiles [0, sinks) and
+        // [lo, hi) those that the run's two stretches (unit_of) hold
+        const int hi = (own.hi_max + kUnit - 1) / kUnit, lo = own.lo_min / kUnit;
+        const int sinks = min(min((int)(((long long)a.sink + kUnit - 1) / kUnit), lo), hi);
+        auto held = [&](int p, int q) { return max(0, min(q, sinks) - p) + max(0, min(q, hi) - max(p, lo)); };
+        const int skip = w.span.t_lo - w.span.n_sink;
+        const int tiles = held(w.j0, min(w.j1, w.span.n_sink)) + held(max(w.j0, w.span.n_sink) + skip, w.j1 + skip);
+        Rec rec;
+        rec.tiles = tiles;
+        rec.nrows = nrows;
+        rec.r0 = r0;
+        rec.row0 = w.q.row0;
+        rec.pos0 = w.q.len - w.q.n;
+        rec.len = w.q.len;
+        rec.h = w.h;
+        rec.whole = w.has_start && w.has_end;
+        rec.run = w.has_start ? 1 : 0;
+        rec.lo_min = own.lo_min;
+        rec.hi_max = own.hi_max;
+        rec.lo_max = own.lo_max;
+        rec.hi_min = own.hi_min;
+        if (!put_record(rec)) return false;
+        if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
+            int* d = a.desc + team * kDesc;
+            d[1] = w.q.row0;
+            d[2] = w.q.n;
+            d[3] = w.h;
+            d[4] = w.rg;
+            d[5] = start.team_of(w.item + max(1, w.span.count) - 1);
+            d[0] = 1;
+        }
+        if (tiles > 0 && !begin(w, r0)) return false;
+        int left = tiles;
+        for (int j = w.j0; left > 0 && j < w.j1; ++j) {
+            const int t = unit_of(w.span, j), key = t * kUnit;
+            if (!wanted(key, kUnit)) continue;
+            const int k0 = key + lane * box;
+            int page = -1;
+            if (lane < (kUnit >> shift) && wanted(k0, box))
+                page = a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)];
+            if (page >= a.c.pages) {
+                record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
+                page = -1;
+            }
+            const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+            int meta = (left == tiles ? kFirst : 0) | (left == 1 ? kLast : 0);
+            --left;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) meta |= ((have >> ((i * 16) >> shift)) & 1u) << i;
+            if ((meta & 0xff) == 0xff && key + kUnit <= own.hi_min &&
+                (key >= own.lo_max || key + kUnit <= min(a.sink, own.lo_min)))
+                meta |= kFull;
+            const long long row = page < 0 ? 0
+                : (((long long)page * a.c.kv_heads + w.h) << a.c.pshift) + (k0 & ((1 << a.c.pshift) - 1));
+            if (!put_tile(meta, t, page, row, have, lane * box, box)) return false;
+        }
+    }
+    return true;
+}
+
 // Where a block keeps the partial result of a segment: run 0 of a team for the item that
 // began in an earlier team, run 1 for the item that it leaves unfinished.
 template <int M>
