@@ -109,7 +109,8 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
 
 template <bool FP8, int M>
 __global__ void __launch_bounds__(kThreads, 2)
-kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ AttnArgs a) {
     using namespace sm100;
     using C = Cfg<FP8, M>;
     constexpr int NH = M / 8;               // 8-row halves in use
@@ -224,7 +225,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int r = hh * 8 + g;
             uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
             if (r < nrows) {
-                const int i = (r0 + r) / a.group;
+                const int i = a.by_group.of(r0 + r);
                 const __nv_bfloat16* p =
                     a.q + (long long)(row0 + i) * a.q_stride + ((long long)rec.h * a.group + (r0 + r - i * a.group)) * 64;
                 const uint4* p4 = reinterpret_cast<const uint4*>(p);
@@ -359,7 +360,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 for (int hh = 0; hh < NH; ++hh) {
                     const int r = hh * 8 + g;
                     int lo = 0, hi = 0;
-                    if (r < nrows) visible(a, len, pos0 + (r0 + r) / a.group, lo, hi);
+                    if (r < nrows) visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
 #pragma unroll
                     for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
@@ -392,7 +393,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             }
                             for (int r = 0; r < nrows; ++r) {
                                 int lo, hi;
-                                visible(a, len, pos0 + (r0 + r) / a.group, lo, hi);
+                                visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
                                 if (key < hi && (key >= lo || key < a.sink))
                                     atomicOr(&ctl.poison[r][g >> 2], cols << ((g & 3) * 8));
                             }
@@ -515,7 +516,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
             if (r < nrows) {
                 if (whole) {
-                    const int i = (r0 + r) / a.group;
+                    const int i = a.by_group.of(r0 + r);
                     const int head = rec.h * a.group + (r0 + r - i * a.group);
                     *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + c4) =
                         make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
@@ -601,7 +602,7 @@ kv_merge_kernel(const AttnArgs a) {
     }
     if (r >= nrows) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int i = (r0 + rb + r) / a.group;
+    const int i = a.by_group.of(r0 + rb + r);
     const int head = h * a.group + (r0 + rb + r - i * a.group);
     *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + 4 * c) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -639,6 +640,7 @@ cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
     a.R = 1;
     a.mr = eight ? 8 : 16;
     a.min_run = 1;
+    a.set_divisors();
     if (eight) {
         e = fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st);
         return e != cudaSuccess ? e : launch_merge<8>(a, st);

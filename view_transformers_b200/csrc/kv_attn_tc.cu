@@ -94,7 +94,8 @@ __device__ __forceinline__ uint32_t bf16_of(uint32_t w, bool upper, __nv_bfloat1
 template <bool FP8>
 __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 2)
 kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+             const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ AttnArgs a) {
     using C = Cfg<FP8>;
     constexpr int NS = C::NS;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -373,7 +374,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             float m_ref = -INFINITY, l = 0.f;
             uint32_t poison0 = 0u, poison1 = 0u;   // columns that met a non-finite value of a key the row sees
             int lo = 0, hi = 0;
-            if (row < rec.nrows) visible(a, rec.len, rec.pos0 + (rec.r0 + row) / a.group, lo, hi);
+            if (row < rec.nrows) visible(a, rec.len, rec.pos0 + a.by_group.of(rec.r0 + row), lo, hi);
             bool ok = true;
             for (int u = 0; u < tiles; ++u, ++U) {
                 const int st = U % NS;
@@ -520,7 +521,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const float inv = l == 0.f ? 0.f : 1.f / l;   // l = 0: nothing seen. NaN stays.
             const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
             const bool whole = rec.whole;
-            const int i = (rec.r0 + row) / a.group;
+            const int i = a.by_group.of(rec.r0 + row);
             const int head = rec.h * a.group + (rec.r0 + row - i * a.group);
             float* part = part_at<128>(a, team, rec.run, member);
 #pragma unroll
@@ -621,6 +622,7 @@ cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
     a.min_run = 2;
     a.R = team_size(a, a.max_teams, max_new);
     a.max_teams /= a.R;
+    a.set_divisors();
     const uint64_t rows = ((uint64_t)a.c.pages * a.c.kv_heads) << a.c.pshift;
     const uint32_t box = a.c.pshift < 7 ? 1u << a.c.pshift : 128u;
     CUtensorMap q, k, v;

@@ -17,6 +17,23 @@ struct CacheArgs {
     const int32_t* kv_len;
 };
 
+// Division of 0 <= n < 2^31 by a divisor that the host knows: with s = ceil(log2 d) and
+// mul = ceil(2^(31 + s) / d), n mul / 2^(31 + s) is at most 2^-s <= 1 / d above n / d. The split of the
+// work is all divisions, one after the other, and a block's first load waits for them.
+struct Div {
+    int d = 1;
+    uint32_t mul = 0, shift = 0;
+    Div() = default;
+    explicit Div(int divisor) : d(divisor) {
+        if (d <= 1) return;
+        int s = 0;
+        while ((1ll << s) < d) ++s;
+        mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+        shift = s - 1;
+    }
+    __device__ __forceinline__ int of(int n) const { return mul == 0u ? n : (int)(__umulhi((uint32_t)n, mul) >> shift); }
+};
+
 struct AttnArgs {
     CacheArgs c;
     int group;                 // query heads per key/value head
@@ -37,7 +54,16 @@ struct AttnArgs {
     int max_teams, R;          // R blocks of a team walk the same keys, each for its own query tile
     int mr;                    // rows of a query tile (at most the M of its kernel)
     int min_run;               // fewest units worth a team of its own
+    Div by_group, by_unit, by_mr, by_R, by_teams, by_run;
     int32_t* status;
+    void set_divisors() {
+        by_group = Div(group);
+        by_unit = Div(unit);
+        by_mr = Div(mr);
+        by_R = Div(R);
+        by_teams = Div(max_teams);
+        by_run = Div(min_run);
+    }
 };
 constexpr int kDesc = 8;       // valid, first row, tokens, kv head, row group, last team
 
@@ -69,7 +95,7 @@ __device__ __forceinline__ void visible(const AttnArgs& a, int len, int p, int& 
         hi = 0;
         return;
     }
-    const long long f = p / a.unit;
+    const long long f = a.by_unit.of(p);
     hi = (int)min((long long)len, (f + 1) * a.unit);
     if (a.window > 0) lo = (int)min((long long)hi, max(0ll, (f - a.window + 1) * a.unit));
 }
@@ -81,7 +107,7 @@ struct Span {
     int lo_min, hi_max;        // positions that some token may see (besides the sink)
     int lo_max, hi_min;        // [lo_max, hi_min) is seen by every token
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& q, int i0, int i1) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, Seq q, int i0, int i1) {
     Span s;
     visible(a, q.len, q.len - q.n + i0, s.lo_min, s.hi_min);
     visible(a, q.len, q.len - q.n + i1, s.lo_max, s.hi_max);
@@ -100,12 +126,11 @@ __device__ __forceinline__ int unit_of(const Span& s, int j) { return j < s.n_si
 // finishes the items that lie inside its run and leaves partial results of the (at most two)
 // that cross its ends, which the merge kernel joins in a fixed order.
 __device__ __forceinline__ int group_count(const AttnArgs& a, const Seq& q) {
-    const int tiles = (q.n * a.group + a.mr - 1) / a.mr;
-    return (tiles + a.R - 1) / a.R;
+    return a.by_R.of(a.by_mr.of(q.n * a.group + a.mr - 1) + a.R - 1);
 }
 // rows [r0, r1) of a sequence's chunk
 __device__ __forceinline__ Span rows_span(const AttnArgs& a, const Seq& q, int r0, int r1) {
-    return span_of(a, q, r0 / a.group, (min(r1, q.n * a.group) - 1) / a.group);
+    return span_of(a, q, a.by_group.of(r0), a.by_group.of(min(r1, q.n * a.group) - 1));
 }
 __device__ __forceinline__ Span group_span(const AttnArgs& a, const Seq& q, int rg) {
     const int r0 = rg * a.R * a.mr;
@@ -114,17 +139,28 @@ __device__ __forceinline__ Span group_span(const AttnArgs& a, const Seq& q, int 
 
 struct Start {
     int s, h, rg;
+    Seq q;                     // sequence s
     int teams;                 // teams that have work
     int item;                  // first unit of the item
     int total;                 // units of all items
-    __device__ __forceinline__ int first_unit(int team) const {
-        const int q = total / teams, r = total - q * teams;
-        return q * team + min(team, r);
-    }
+    int run, wide;             // the first `wide` teams get run + 1 units, the others run
+    __device__ __forceinline__ int first_unit(int team) const { return run * team + min(team, wide); }
     // the team that holds unit u
     __device__ __forceinline__ int team_of(int u) const {
-        const int q = total / teams, r = total - q * teams, wide = r * (q + 1);
-        return u < wide ? u / (q + 1) : r + (u - wide) / q;
+        const int w = wide * (run + 1);
+        return u < w ? u / (run + 1) : wide + (u - w) / run;
+    }
+    __device__ __forceinline__ void deal(const AttnArgs& a, int units) {
+        total = units;
+        const int most = a.by_run.of(units);            // teams that the work is worth
+        teams = max(1, min(a.max_teams, most));
+        run = most >= a.max_teams ? a.by_teams.of(units) : a.min_run;
+        if (teams == 1) run = units;
+        wide = units - run * teams;
+        if (wide > teams) {                             // min_run units each leave more than one a team
+            run = units / teams;
+            wide = units - run * teams;
+        }
     }
 };
 
@@ -163,23 +199,16 @@ __device__ __forceinline__ int head_units_warp(const AttnArgs& a, const Seq& q, 
     for (int g = lane; g < ng; g += 32) u += max(1, group_span(a, q, g).count);
     return lane_sum(u);
 }
-// teams that the total is worth, then the item of the first unit of `team`, which lies in
-// sequence r.s at unit `base` (whole warp)
-__device__ __forceinline__ void find_item(const AttnArgs& a, const Seq& q, int base, int per_head, int u0, int lane,
-                                          Start& r) {
+// the item of unit u0, which lies in the sequence r.q that starts at unit `base` (whole warp)
+__device__ __forceinline__ void find_item(const AttnArgs& a, int base, int per_head, int u0, int lane, Start& r) {
     r.h = (u0 - base) / per_head;
     r.item = base + r.h * per_head;
     r.rg = 0;
+    const int ng = group_count(a, r.q);
+    if (ng == 1) return;
     int rest = u0 - r.item;
-    const int ng = group_count(a, q);
-    if (a.unit == 0) {
-        const int each = per_head / ng;
-        r.rg = rest / each;
-        r.item += r.rg * each;
-        return;
-    }
     for (int g0 = 0; g0 < ng; g0 += 32) {
-        const int own = g0 + lane < ng ? max(1, group_span(a, q, g0 + lane).count) : 0;
+        const int own = g0 + lane < ng ? max(1, group_span(a, r.q, g0 + lane).count) : 0;
         const int v = lane_scan(own, lane);
         const unsigned in = __ballot_sync(0xffffffffu, g0 + lane < ng && rest < v);
         if (in) {
@@ -196,15 +225,19 @@ __device__ __forceinline__ void find_item(const AttnArgs& a, const Seq& q, int b
 
 constexpr int kMostUnits = 1 << 30;
 
+static __device__ __noinline__ Start plan_many(const AttnArgs& a, int team, int* pre, int* list, Start* st);
+
 // The split of the work, for this block's team. Up to 32 sequences: every warp by itself,
 // without shared memory or a barrier. More: the whole block, through pre (seqs + 1 ints), list
 // (seqs + 1 ints) and *st in shared memory. Work beyond 2^30 units is refused.
 __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int* list, Start* st) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int S = a.c.seqs;
+    if (S > 32) return plan_many(a, team, pre, list, st);
     Start r;
     r.s = r.h = r.rg = r.item = 0;
-    if (S <= 32) {
+    r.q.row0 = r.q.n = r.q.len = 0;
+    {
         Seq q;
         q.row0 = q.n = q.len = 0;
         if (lane < S) q = load_seq(a.c, a.cu, a.rows, lane, a.status, blockIdx.x == 0 && warp == 0);
@@ -221,26 +254,28 @@ __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int
         }
         const float most = (float)u * (float)a.c.kv_heads;   // 32 such sums stay inside 2^31
         const bool over = __any_sync(0xffffffffu, most > (float)(kMostUnits / 32));
+        const int head = u;
         u *= a.c.kv_heads;
         const int v = lane_scan(u, lane);
-        r.total = __shfl_sync(0xffffffffu, v, 31);
-        if (over) {
-            if (tid == 0) record_error(a.status, BSA_ERR_UNSUPPORTED);
-            r.total = 0;
-        }
-        r.teams = min(a.max_teams, max(1, r.total / a.min_run));
+        const int total = __shfl_sync(0xffffffffu, v, 31);
+        if (over && threadIdx.x == 0) record_error(a.status, BSA_ERR_UNSUPPORTED);
+        r.deal(a, over ? 0 : total);
         const int u0 = team < r.teams ? r.first_unit(team) : r.total;
         const unsigned in = __ballot_sync(0xffffffffu, v > u0 && u > 0);
         if (in && u0 < r.total) {
             r.s = __ffs(in) - 1;
-            Seq o;
-            o.row0 = __shfl_sync(0xffffffffu, q.row0, r.s);
-            o.n = __shfl_sync(0xffffffffu, q.n, r.s);
-            o.len = __shfl_sync(0xffffffffu, q.len, r.s);
-            find_item(a, o, __shfl_sync(0xffffffffu, v - u, r.s), __shfl_sync(0xffffffffu, u, r.s) / a.c.kv_heads, u0, lane, r);
+            r.q.row0 = __shfl_sync(0xffffffffu, q.row0, r.s);
+            r.q.n = __shfl_sync(0xffffffffu, q.n, r.s);
+            r.q.len = __shfl_sync(0xffffffffu, q.len, r.s);
+            find_item(a, __shfl_sync(0xffffffffu, v - u, r.s), __shfl_sync(0xffffffffu, head, r.s), u0, lane, r);
         }
         return r;
     }
+}
+
+static __device__ __noinline__ Start plan_many(const AttnArgs& a, int team, int* pre, int* list, Start* st) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    const int S = a.c.seqs;
     if (tid == 0) list[S] = 0;
     __syncthreads();
     for (int s = tid; s < S; s += nt) {
@@ -257,6 +292,9 @@ __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int
     }
     __syncthreads();
     if (warp == 0) {
+        Start r;
+        r.s = r.h = r.rg = r.item = 0;
+        r.q.row0 = r.q.n = r.q.len = 0;
         int base = 0;
         bool over = false;
         for (int s0 = 0; s0 < S; s0 += 32) {
@@ -274,8 +312,7 @@ __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int
         }
         if (lane == 0) pre[S] = base;
         __syncwarp();
-        r.total = base;
-        r.teams = min(a.max_teams, max(1, base / a.min_run));
+        r.deal(a, base);
         const int u0 = team < r.teams ? r.first_unit(team) : base;
         if (u0 < base) {
             int lo = 0, hi = S;                     // the last sequence with pre[s] <= u0
@@ -284,8 +321,8 @@ __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int
                 if (pre[mid] <= u0) lo = mid; else hi = mid;
             }
             r.s = lo;
-            find_item(a, load_seq(a.c, a.cu, a.rows, lo, nullptr, false), pre[lo], (pre[lo + 1] - pre[lo]) / a.c.kv_heads,
-                      u0, lane, r);
+            r.q = load_seq(a.c, a.cu, a.rows, lo, nullptr, false);
+            find_item(a, pre[lo], (pre[lo + 1] - pre[lo]) / a.c.kv_heads, u0, lane, r);
         }
         if (lane == 0) *st = r;
     }
@@ -310,9 +347,8 @@ struct Walk {
         s = st.s;
         h = st.h;
         rg = st.rg;
-        q.row0 = q.n = q.len = 0;
-        ng = 0;
-        if (u < u1) enter();
+        q = st.q;
+        ng = u < u1 ? group_count(a, q) : 0;
     }
     __device__ __forceinline__ void enter() {
         q = load_seq(a.c, a.cu, a.rows, s, nullptr, false);
@@ -374,7 +410,7 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
         const int r0 = (w.rg * a.R + member) * a.mr;
         const int nrows = min(a.mr, w.q.n * a.group - r0);
         if (nrows <= 0) continue;
-        const Span own = rows_span(a, w.q, r0, r0 + a.mr);
+        const Span own = a.R == 1 ? w.span : rows_span(a, w.q, r0, r0 + a.mr);
         auto wanted = [&](int k0, int n) { return k0 < own.hi_max && (k0 + n > own.lo_min || k0 < a.sink); };
         // how many of the run's tiles this query tile needs: of the tiles [0, sinks) and
         // [lo, hi) those that the run's two stretches (unit_of) hold
@@ -398,24 +434,28 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
         rec.lo_max = own.lo_max;
         rec.hi_min = own.hi_min;
         if (!put_record(rec)) return false;
-        if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
-            int* d = a.desc + team * kDesc;
-            d[1] = w.q.row0;
-            d[2] = w.q.n;
-            d[3] = w.h;
-            d[4] = w.rg;
-            d[5] = start.team_of(w.item + max(1, w.span.count) - 1);
-            d[0] = 1;
-        }
         if (tiles > 0 && !begin(w, r0)) return false;
+        // page ids come 32 boxes at a time, the next ones while these are handed out: lane i holds
+        // box i % boxes of the run's tile jb + i / boxes
+        const int boxes = kUnit >> shift, per = 32 / boxes;
+        auto fetch = [&](int jb) {
+            const int j = jb + (lane >> (7 - shift));
+            const int k0 = unit_of(w.span, j) * kUnit + (lane & (boxes - 1)) * box;
+            return j < w.j1 && wanted(k0, box) ? a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)] : -1;
+        };
+        int ids = fetch(w.j0), ahead = fetch(w.j0 + per), jb = w.j0;
         int left = tiles;
         for (int j = w.j0; left > 0 && j < w.j1; ++j) {
+            if (j - jb == per) {
+                jb = j;
+                ids = ahead;
+                ahead = fetch(j + per);
+            }
             const int t = unit_of(w.span, j), key = t * kUnit;
             if (!wanted(key, kUnit)) continue;
             const int k0 = key + lane * box;
-            int page = -1;
-            if (lane < (kUnit >> shift) && wanted(k0, box))
-                page = a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)];
+            int page = __shfl_sync(0xffffffffu, ids, (j - jb) * boxes + (lane & (boxes - 1)));
+            if (lane >= boxes) page = -1;
             if (page >= a.c.pages) {
                 record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
                 page = -1;
@@ -431,6 +471,15 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
             const long long row = page < 0 ? 0
                 : (((long long)page * a.c.kv_heads + w.h) << a.c.pshift) + (k0 & ((1 << a.c.pshift) - 1));
             if (!put_tile(meta, t, page, row, have, lane * box, box)) return false;
+        }
+        if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
+            int* d = a.desc + team * kDesc;
+            d[1] = w.q.row0;
+            d[2] = w.q.n;
+            d[3] = w.h;
+            d[4] = w.rg;
+            d[5] = start.team_of(w.item + max(1, w.span.count) - 1);
+            d[0] = 1;
         }
     }
     return true;
