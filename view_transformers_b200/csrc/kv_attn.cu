@@ -6,21 +6,26 @@
 //   keys a row sees, with a running reference m that is raised only when some x exceeds it by 8.
 //
 // With few rows the keys and values are read once and nothing else matters: the bound is HBM
-// (128 bytes a row of K or V, 65 in e4m3), and for e4m3 the instructions that turn codes into
-// operands. So the matrix instruction is the small one, with M rows (8 or 16 of its 16):
+// (128 bytes a row of K or V, 65 in e4m3). So the matrix instruction is the small one (mma.sync),
+// with M rows (8 or 16 of its 16):
 //   - one warp gathers tiles of 128 keys from their pages by TMA into a ring of stages, running
-//     ahead across items; eight warps take 16 keys of each tile and keep their own m, l and O, and
-//     meet at the end of an item;
-//   - a dot product does not care about the order of its terms, so the lane that must hold two
+//     ahead across items; eight warps share the tiles, each with its own m, l and O, and meet at
+//     the end of an item;
+//   - a dot product does not care about the order of its terms, so the lane that must hold
 //     neighbouring d of key g takes 16 neighbouring bytes of that key instead, and Q is loaded in
-//     the same order; P.V's columns are dealt out so that a lane needs 8 neighbouring d of four
+//     the same order; P.V's columns are dealt out so that a lane needs 8 neighbouring d of its
 //     keys. All reads of a stage are 8 or 16 bytes wide and free of bank conflicts: bf16 tiles are
 //     swizzled by TMA (16-byte chunk c of row r at c ^ (r & 7)); e4m3 tiles are not, and the keys
-//     are numbered so that the four rows that a lane quad needs lie next to each other;
-//   - e4m3 codes become f16 by one conversion for Q.K (Q is scaled to f16 per row, exact for
-//     elements within 2^-28 of the row's largest); for P.V their bits are moved into a bf16 as
-//     they are, 2^-120 times the value. The rows' scales go into the scores and into P, which bf16
-//     holds without loss, and P carries 2^100 so that nothing underflows.
+//     are numbered so that the four rows that a lane quad needs lie next to each other.
+// bf16: a warp takes 16 keys of each tile, P is rounded to bf16.
+// e4m3: a warp takes 32 keys of every second tile. The bound is then the integer pipe (two clocks an
+// instruction), so the codes become f16 by the one conversion there is and their scales go
+// elsewhere: a K row's into the scores; a V row's, 2^e, into P: w_j = p_j 2^(e_j), rounded to f16
+// relative to the largest w of the warp's 32 keys (full precision over 28 binades, whatever the
+// scales), and the step's product is added to O in fp32 at its own scale. Q is f16 too, scaled by a
+// power of two per row, exact for elements within 2^-28 of the row's largest. (The e4m3 form of
+// mma.sync, with Q and P in two parts each, measured slower: 184 against 165 us with bf16 operands on
+// 32 ragged streams.)
 #include "kv_cache.cuh"
 #include "sm100.cuh"
 #include "tma_map.cuh"
@@ -36,25 +41,25 @@ constexpr int kThreads = kWarps * 32 + 32;           // and the producer's warp
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLift = 100.f;                       // e4m3: P carries 2^100 ...
-constexpr float kBack = 0x1p120f;                    // ... as does l, and V's operand is 2^-120 V
 
 template <bool FP8, int M>
 struct Cfg {
     // e4m3: K, V, and their scales; bf16: K and V. Two blocks share an SM.
     static constexpr uint32_t kV = FP8 ? 8192 : 16384;
     static constexpr uint32_t kStage = FP8 ? 2 * 8192 + 2 * 128 : 2 * 16384;
-    static constexpr int NS = FP8 ? (M == 8 ? 5 : 4) : (M == 8 ? 3 : 2);
+    // e4m3: even, so that a stage always belongs to the same half of the warps
+    static constexpr int NS = FP8 ? 4 : (M == 8 ? 3 : 2);
+    static constexpr int kSharers = FP8 ? 4 : 8;                      // warps that read a tile
     static constexpr uint32_t kMerge = NS * kStage;                   // [warp][row][64 + 2]
     static constexpr uint32_t kCtl = kMerge + kWarps * M * 66 * 4;
 };
 
 template <int M>
 struct Ctl {
-    uint64_t full[5], empty[5];
+    uint64_t full[4], empty[4];
     uint64_t rec_full[2], rec_empty[2], meet;
     Rec rec[2];
-    int meta[5], tile[5];
+    int meta[4], tile[4];
     uint32_t poison[M][2];                  // columns of a row that met a NaN or infinite value
     int abort;
     Start start;
@@ -96,12 +101,6 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
-// byte j of two words of codes to the bf16 pair 2^-120 times their values: sign, then the 7 bits
-// of exponent and mantissa moved into a bf16's (subnormal codes become subnormal bf16)
-__device__ __forceinline__ uint32_t bf16_pair(uint32_t a, uint32_t b, int j) {
-    const uint32_t y = __byte_perm(a, b, j | j << 4 | (4 + j) << 8 | (4 + j) << 12);
-    return ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
-}
 
 __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -123,7 +122,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (tid == 0) {
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(&ctl.full[s], 1);
-            mbar_init(&ctl.empty[s], kWarps);
+            mbar_init(&ctl.empty[s], C::kSharers);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl.rec_full[s], 1);
@@ -218,8 +217,9 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (tiles < 0) break;
         const int nrows = rec.nrows, r0 = rec.r0, row0 = rec.row0, pos0 = rec.pos0, len = rec.len;
         // ---------------------------------------------------------------- Q
+        // k-step ks takes the words qf[ks][hh] and qf[ks][NH + hh] of rows 8 hh + g
         uint32_t qf[4][2 * NH];
-        float rowf[NH];                     // x = score * rowf
+        float rowf[NH];                     // x = score * rowf (e4m3: times the key's scale)
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
             const int r = hh * 8 + g;
@@ -245,8 +245,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const float inv = pow2_of(254 - e);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    wds[k] = sm100::pack_half2(__uint_as_float(wds[k] << 16) * inv,
-                                               __uint_as_float(wds[k] & 0xffff0000u) * inv);
+                    wds[k] = pack_half2(__uint_as_float(wds[k] << 16) * inv, __uint_as_float(wds[k] & 0xffff0000u) * inv);
                 rowf[hh] = kScaleLog2 * pow2_of(e);
             }
 #pragma unroll
@@ -260,7 +259,6 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-        constexpr float kUp = FP8 ? kLift : 0.f;   // m is kUp below the largest score (log2 units)
         float m[NH], l[NH];
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
@@ -268,6 +266,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             l[hh] = 0.f;
         }
 
+        if constexpr (!FP8) {
         for (int u = 0; u < tiles; ++u, ++U) {
             const int s = U % C::NS;
             if (!warp_wait(&ctl.full[s], (U / C::NS) & 1, abort, a.status)) return;
@@ -281,75 +280,35 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 if (lane == 0) mbar_arrive(&ctl.empty[s]);
                 continue;
             }
-            // key of the warp's 16 that column x (0 .. 7) of the scores' half jj stands for
-            auto key_of = [](int jj, int x) {
-                return FP8 ? jj * 8 + (x & 1 ? 4 + ((x >> 1) ^ 1) : x >> 1) : jj * 8 + x;
-            };
+            // column x (0 .. 7) of the scores' half jj stands for key jj * 8 + x of the warp's 16
             const uint32_t src = smem_u32(smem + s * C::kStage);
             // ------------------------------------------------------------ scores
             float x[2][4];
-            float ksc[2][2], vsc[2][2];
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) x[jj][c] = 0.f;
-                const int r = warp * 16 + key_of(jj, g);
-                if (!FP8) {
-                    const uint4 k0 = lds16(src + r * 128 + (((2 * t) ^ (r & 7)) << 4));
-                    const uint4 k1 = lds16(src + r * 128 + (((2 * t + 1) ^ (r & 7)) << 4));
-                    const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+                const int r = warp * 16 + jj * 8 + g;
+                const uint4 k0 = lds16(src + r * 128 + (((2 * t) ^ (r & 7)) << 4));
+                const uint4 k1 = lds16(src + r * 128 + (((2 * t + 1) ^ (r & 7)) << 4));
+                const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(x[jj], qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
-                                 kw[2 * ks], kw[2 * ks + 1]);
-                } else {
-                    const uint4 k0 = lds16(src + r * 64 + t * 16);
-                    const uint32_t kw[4] = {k0.x, k0.y, k0.z, k0.w};
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(x[jj], qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
+                             kw[2 * ks], kw[2 * ks + 1]);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16(x[jj], qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
-                                half2_of(kw[ks], false), half2_of(kw[ks], true));
-                }
-            }
-            if (FP8) {
-                // scale bytes of the warp's keys: those of a lane's columns are bytes t, 4 + (t ^ 1) of
-                // each half. 255 << 23 is infinite, and inf - inf makes the score NaN.
-                const uint4 kb4 = lds16(src + 16384 + warp * 16), vb4 = lds16(src + 16384 + 128 + warp * 16);
-                const uint32_t kw[4] = {kb4.x, kb4.y, kb4.z, kb4.w}, vw[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int at = c ? t ^ 1 : t;
-                        ksc[jj][c] = __uint_as_float(((kw[2 * jj + c] >> (8 * at)) << 23) & 0x7f800000u);
-                        vsc[jj][c] = __uint_as_float(((vw[2 * jj + c] >> (8 * at)) << 23) & 0x7f800000u);
-                        const float zero = ksc[jj][c] - ksc[jj][c];
-#pragma unroll
-                        for (int hh = 0; hh < NH; ++hh)
-                            x[jj][2 * hh + c] = fmaf(x[jj][2 * hh + c], ksc[jj][c] * rowf[hh], zero);
-                    }
-            } else {
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                    for (int c = 0; c < 2 * NH; ++c) x[jj][c] *= kScaleLog2;
+                for (int c = 0; c < 2 * NH; ++c) x[jj][c] *= kScaleLog2;
             }
             // ------------------------------------------------------------ V, and what is seen
-            uint32_t vw[4][4];              // keys of the lane's four columns: 8 values (bf16) or codes
+            uint32_t vw[4][4];              // 8 values of the lane's four keys
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = warp * 16 + key_of(i >> 1, 2 * t + (i & 1));
-                if (!FP8) {
-                    const uint4 v = lds16(src + C::kV + r * 128 + ((g ^ (r & 7)) << 4));
-                    vw[i][0] = v.x;
-                    vw[i][1] = v.y;
-                    vw[i][2] = v.z;
-                    vw[i][3] = v.w;
-                } else {
-                    const uint2 v = lds8(src + C::kV + r * 64 + g * 8);
-                    vw[i][0] = v.x;
-                    vw[i][1] = v.y;
-                }
+                const int r = warp * 16 + (i >> 1) * 8 + 2 * t + (i & 1);
+                const uint4 v = lds16(src + C::kV + r * 128 + ((g ^ (r & 7)) << 4));
+                vw[i][0] = v.x;
+                vw[i][1] = v.y;
+                vw[i][2] = v.z;
+                vw[i][3] = v.w;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.empty[s]);
@@ -365,38 +324,36 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const int key = kb + key_of(jj, 2 * t + c);
+                            const int key = kb + jj * 8 + 2 * t + c;
                             if (key < hi && (key >= lo || key < a.sink)) seen |= 1u << (jj * 4 + 2 * hh + c);
                         }
                 }
-                if (!FP8) {
-                    // P = 0 does not silence a NaN: non-finite values are taken out of V and marked
-                    // in the rows that see them (none, past the end)
+                // P = 0 does not silence a NaN: non-finite values are taken out of V and marked
+                // in the rows that see them (none, past the end)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = kb + key_of(i >> 1, 2 * t + (i & 1));
-                        bool bad = false;
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + (i >> 1) * 8 + 2 * t + (i & 1);
+                    bool bad = false;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) bad |= has_nonfinite(vw[i][k]);
-                        if (bad) {
-                            uint32_t cols = 0u;
+                    for (int k = 0; k < 4; ++k) bad |= has_nonfinite(vw[i][k]);
+                    if (bad) {
+                        uint32_t cols = 0u;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if ((vw[i][k] & 0x7f80u) == 0x7f80u) {
-                                    cols |= 1u << (2 * k);
-                                    vw[i][k] &= 0xffff0000u;
-                                }
-                                if ((vw[i][k] & 0x7f800000u) == 0x7f800000u) {
-                                    cols |= 2u << (2 * k);
-                                    vw[i][k] &= 0xffffu;
-                                }
+                        for (int k = 0; k < 4; ++k) {
+                            if ((vw[i][k] & 0x7f80u) == 0x7f80u) {
+                                cols |= 1u << (2 * k);
+                                vw[i][k] &= 0xffff0000u;
                             }
-                            for (int r = 0; r < nrows; ++r) {
-                                int lo, hi;
-                                visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
-                                if (key < hi && (key >= lo || key < a.sink))
-                                    atomicOr(&ctl.poison[r][g >> 2], cols << ((g & 3) * 8));
+                            if ((vw[i][k] & 0x7f800000u) == 0x7f800000u) {
+                                cols |= 2u << (2 * k);
+                                vw[i][k] &= 0xffffu;
                             }
+                        }
+                        for (int r = 0; r < nrows; ++r) {
+                            int lo, hi;
+                            visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
+                            if (key < hi && (key >= lo || key < a.sink))
+                                atomicOr(&ctl.poison[r][g >> 2], cols << ((g & 3) * 8));
                         }
                     }
                 }
@@ -412,7 +369,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {
                 top[hh] = fmaxf(fmaxf(x[0][2 * hh], x[0][2 * hh + 1]), fmaxf(x[1][2 * hh], x[1][2 * hh + 1]));
-                need |= top[hh] > m[hh] + (kRescale + kUp);
+                need |= top[hh] > m[hh] + kRescale;
             }
             if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -420,7 +377,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     float n = top[hh];
                     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
                     n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
-                    n = fmaxf(n - kUp, m[hh]);
+                    n = fmaxf(n, m[hh]);
                     const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
                     m[hh] = n;
                     l[hh] *= f;
@@ -437,34 +394,202 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const float ref = m[hh] == -INFINITY ? 0.f : m[hh];
 #pragma unroll
                 for (int jj = 0; jj < 2; ++jj) {
-                    float p0 = ex2_approx(x[jj][2 * hh] - ref), p1 = ex2_approx(x[jj][2 * hh + 1] - ref);
+                    const float p0 = ex2_approx(x[jj][2 * hh] - ref), p1 = ex2_approx(x[jj][2 * hh + 1] - ref);
                     l[hh] += p0 + p1;
-                    if (FP8) {
-                        p0 *= vsc[jj][0];
-                        p1 *= vsc[jj][1];
-                        if (!all) {         // a masked P is 0, whatever the scale byte holds
-                            if (!((seen >> (jj * 4 + 2 * hh)) & 1u)) p0 = 0.f;
-                            if (!((seen >> (jj * 4 + 2 * hh + 1)) & 1u)) p1 = 0.f;
-                        }
-                    }
                     pf[jj][hh] = pack_bf16(p0, p1);
                 }
             }
             // ------------------------------------------------------------ O += P V
             const uint32_t p1a = NH == 2 ? pf[0][NH - 1] : 0u, p1b = NH == 2 ? pf[1][NH - 1] : 0u;
-            if (!FP8) {
 #pragma unroll
-                for (int j8 = 0; j8 < 8; ++j8) {
-                    const uint32_t sel = j8 & 1 ? 0x7632u : 0x5410u;
-                    mma_bf16(o[j8], pf[0][0], p1a, pf[1][0], p1b, __byte_perm(vw[0][j8 >> 1], vw[1][j8 >> 1], sel),
-                             __byte_perm(vw[2][j8 >> 1], vw[3][j8 >> 1], sel));
-                }
-            } else {
-#pragma unroll
-                for (int j8 = 0; j8 < 8; ++j8)
-                    mma_bf16(o[j8], pf[0][0], p1a, pf[1][0], p1b, bf16_pair(vw[0][j8 >> 2], vw[1][j8 >> 2], j8 & 3),
-                             bf16_pair(vw[2][j8 >> 2], vw[3][j8 >> 2], j8 & 3));
+            for (int j8 = 0; j8 < 8; ++j8) {
+                const uint32_t sel = j8 & 1 ? 0x7632u : 0x5410u;
+                mma_bf16(o[j8], pf[0][0], p1a, pf[1][0], p1b, __byte_perm(vw[0][j8 >> 1], vw[1][j8 >> 1], sel),
+                         __byte_perm(vw[2][j8 >> 1], vw[3][j8 >> 1], sel));
             }
+        }
+        } else {
+        for (int u = 0; u < tiles; ++u, ++U) {
+            if ((U & 1) != warp >> 2) continue;   // the other half's tile
+            const int s = U % C::NS, sub = warp & 3;
+            if (!warp_wait(&ctl.full[s], (U / C::NS) & 1, abort, a.status)) return;
+            const int meta = ctl.meta[s], kb = ctl.tile[s] * kUnit + sub * 32;
+            const int there = (meta >> (2 * sub)) & 3;   // pages of the two 16-key halves
+            const bool want = there != 0 &&
+                              ((meta & kFull) || (kb < rec.hi_max && (kb + 32 > rec.lo_min || kb < a.sink)));
+            const bool all = (meta & kFull) || (there == 3 && kb + 32 <= rec.hi_min &&
+                                                (kb >= rec.lo_max || kb + 32 <= min(a.sink, rec.lo_min)));
+            if (!want) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.empty[s]);
+                continue;
+            }
+            // column c of the scores' eighth n stands for key 8 n + c / 2 (c even), 8 n + 4 + (c / 2 ^ 1)
+            // (odd): pairs of columns differ in parity and equal columns of a quad lie together
+            const uint32_t src = smem_u32(smem + s * C::kStage);
+            const int kg = g & 1 ? 4 + ((g >> 1) ^ 1) : g >> 1;   // key of column g
+            const int k1 = 4 + (t ^ 1);                           // key of column 2 t + 1; 2 t: t
+            // ------------------------------------------------------------ scores
+            float x[4][2 * NH];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint4 kw = lds16(src + (sub * 32 + 8 * n + kg) * 64 + t * 16);
+                const uint32_t kc[4] = {kw.x, kw.y, kw.z, kw.w};
+                float h[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f16(h, qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
+                            half2_of(kc[ks], false), half2_of(kc[ks], true));
+#pragma unroll
+                for (int c = 0; c < 2 * NH; ++c) x[n][c] = h[c];
+            }
+            // scales: x takes the K row's as a factor (byte 255 gives inf, and inf - inf makes the score
+            // NaN), y = x + the V row's exponent
+            float ve[4][2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint4 kb4 = lds16(src + 16384 + sub * 32 + half * 16);
+                const uint4 vb4 = lds16(src + 16384 + 128 + sub * 32 + half * 16);
+                const uint32_t kw[4] = {kb4.x, kb4.y, kb4.z, kb4.w}, vw[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int n = 2 * half + i;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t at = c ? t ^ 1 : t;
+                        const float ks = __uint_as_float(__byte_perm(kw[2 * i + c], 0u, 0x0444u | at << 12) >> 1);
+                        const float zero = ks - ks;
+#pragma unroll
+                        for (int hh = 0; hh < NH; ++hh) x[n][2 * hh + c] = fmaf(x[n][2 * hh + c], ks * rowf[hh], zero);
+                        // 2^23 + byte, as a float
+                        ve[n][c] = __uint_as_float(__byte_perm(vw[2 * i + c], 0x4b000000u, 0x7650u | at)) - 8388735.f;
+                    }
+                }
+            }
+            // ------------------------------------------------------------ V
+            uint2 vc[2][4];                   // codes of d 8 g .. 8 g + 7 for the lane's eight keys
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    vc[half][i] = lds8(src + C::kV + (sub * 32 + half * 16 + (i >> 1) * 8 + (i & 1 ? k1 : t)) * 64 + g * 8);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.empty[s]);
+            // ------------------------------------------------------------ what is seen
+            if (!all) {
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    const int r = hh * 8 + g;
+                    int lo = 0, hi = 0;
+                    if (r < nrows) visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int key = kb + 8 * n + (c ? k1 : t);
+                            if (!(key < hi && (key >= lo || key < a.sink) && ((there >> (n >> 1)) & 1)))
+                                x[n][2 * hh + c] = -INFINITY;
+                        }
+                }
+                // stale memory may hold NaN codes (a written row never does: NaN is in its scale)
+                auto clean = [](uint32_t& w) {
+                    w &= ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 255u);
+                };
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        clean(vc[half][i].x);
+                        clean(vc[half][i].y);
+                    }
+            }
+            // ------------------------------------------------------------ softmax
+            float top[NH], high = ve[0][0];   // of x per row; of the V exponents
+            bool need = false;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) high = fmaxf(high, fmaxf(ve[n][0], ve[n][1]));
+            if (high > 100.f) {               // a V row that stands for NaN (or stale memory that is masked)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (ve[n][c] > 100.f) ve[n][c] = __uint_as_float(0x7fc00000u);
+            }
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                top[hh] = fmaxf(x[0][2 * hh], x[0][2 * hh + 1]);
+#pragma unroll
+                for (int n = 1; n < 4; ++n) top[hh] = fmaxf(top[hh], fmaxf(x[n][2 * hh], x[n][2 * hh + 1]));
+                need |= top[hh] > m[hh] + kRescale;
+            }
+            if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    float n = top[hh];
+                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
+                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
+                    n = fmaxf(n, m[hh]);
+                    const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
+                    m[hh] = n;
+                    l[hh] *= f;
+#pragma unroll
+                    for (int j8 = 0; j8 < 8; ++j8) {
+                        o[j8][2 * hh] *= f;
+                        o[j8][2 * hh + 1] *= f;
+                    }
+                }
+            }
+            uint32_t pf[4][NH];               // w of the lane's two keys of each eighth
+            float back[NH];
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                const float ref = m[hh] == -INFINITY ? 0.f : m[hh];
+                float y[4][2], yt = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float xv = x[n][2 * hh + c];
+                        sum += ex2_approx(xv - ref);
+                        // a masked score stays -infinity, whatever the scale byte holds
+                        y[n][c] = all || xv != -INFINITY ? xv + ve[n][c] : -INFINITY;
+                        yt = fmaxf(yt, y[n][c]);
+                    }
+                l[hh] += sum;
+                yt = fmaxf(yt, __shfl_xor_sync(0xffffffffu, yt, 1));
+                yt = fmaxf(yt, __shfl_xor_sync(0xffffffffu, yt, 2));
+                const float base = yt == -INFINITY ? 0.f : yt - 14.f;   // the largest w is 2^14
+                back[hh] = ex2_approx(base - ref);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    pf[n][hh] = pack_half2(ex2_approx(y[n][0] - base), ex2_approx(y[n][1] - base));
+            }
+            // ------------------------------------------------------------ O += 2^(base - m) w V
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t ab[2], cd[2];    // d 4 k + 2 z and one further, two keys each
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint2(&v)[4] = vc[half];
+                        const uint32_t sel = z ? 0x7362u : 0x5140u;
+                        ab[half] = k ? __byte_perm(v[0].y, v[1].y, sel) : __byte_perm(v[0].x, v[1].x, sel);
+                        cd[half] = k ? __byte_perm(v[2].y, v[3].y, sel) : __byte_perm(v[2].x, v[3].x, sel);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float h[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            mma_f16(h, pf[2 * half][0], NH == 2 ? pf[2 * half][NH - 1] : 0u, pf[2 * half + 1][0],
+                                    NH == 2 ? pf[2 * half + 1][NH - 1] : 0u, half2_of(ab[half], y), half2_of(cd[half], y));
+                        const int j8 = 4 * k + 2 * z + y;
+#pragma unroll
+                        for (int c = 0; c < 2 * NH; ++c) o[j8][c] = fmaf(h[c], back[c >> 1], o[j8][c]);
+                    }
+                }
+        }
         }
 
         // -------------------------------------------------------------------- the block's warps
@@ -506,7 +631,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 acc[3] += f * v.w;
             }
             // l = 0: nothing seen. NaN stays.
-            const float inv = (ll == 0.f ? 0.f : 1.f / ll) * (FP8 ? kBack : 1.f);
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
             const uint32_t bad = ctl.poison[r][c4 >> 5] >> (c4 & 31);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
