@@ -8,27 +8,27 @@
 // With few rows the keys and values are read once and nothing else matters: the bound is HBM
 // (128 bytes a row of K or V, 65 in e4m3). So the matrix instruction is the small one (mma.sync),
 // with M rows (8 or 16 of its 16):
-//   - one warp gathers tiles of 128 keys from their pages by TMA into a ring of stages, running
-//     ahead across items; eight warps share the tiles, each with its own m, l and O, and meet at
-//     the end of an item;
+//   - a block is eight warps that work alone until an item ends: each takes every eighth group of
+//     16 (bf16) or 32 (e4m3) keys, copies them asynchronously into a ring of its own (pages two
+//     groups ahead, page ids 32 groups ahead, both across items) and keeps its own m, l and O.
+//     (One producer warp with TMA for all eight was measured: at 1,400 to 2,000 clocks a tile it
+//     kept e4m3 at 61% of HBM.)
 //   - a dot product does not care about the order of its terms, so the lane that must hold
 //     neighbouring d of key g takes 16 neighbouring bytes of that key instead, and Q is loaded in
 //     the same order; P.V's columns are dealt out so that a lane needs 8 neighbouring d of its
-//     keys. All reads of a stage are 8 or 16 bytes wide and free of bank conflicts: bf16 tiles are
-//     swizzled by TMA (16-byte chunk c of row r at c ^ (r & 7)); e4m3 tiles are not, and the keys
-//     are numbered so that the four rows that a lane quad needs lie next to each other.
-// bf16: a warp takes 16 keys of each tile, P is rounded to bf16.
-// e4m3: a warp takes 32 keys of every second tile. The bound is then the integer pipe (two clocks an
-// instruction), so the codes become f16 by the one conversion there is and their scales go
-// elsewhere: a K row's into the scores; a V row's, 2^e, into P: w_j = p_j 2^(e_j), rounded to f16
-// relative to the largest w of the warp's 32 keys (full precision over 28 binades, whatever the
-// scales), and the step's product is added to O in fp32 at its own scale. Q is f16 too, scaled by a
-// power of two per row, exact for elements within 2^-28 of the row's largest. (The e4m3 form of
-// mma.sync, with Q and P in two parts each, measured slower: 184 against 165 us with bf16 operands on
-// 32 ragged streams.)
+//     keys. All reads of a stage are 8 or 16 bytes wide and free of bank conflicts: bf16 rows are
+//     swizzled as they are copied (16-byte chunk c of row r at c ^ (r & 7)); e4m3 rows are not, and
+//     the keys are numbered so that the four rows that a lane quad needs lie next to each other.
+// bf16: P is rounded to bf16.
+// e4m3: the integer pipe (two clocks an instruction) is nearest to a bound, so the codes become f16
+// by the one conversion there is and their scales go elsewhere: a K row's into the scores; a V
+// row's, 2^e, into P: w_j = p_j 2^(e_j), rounded to f16 relative to the largest w of the group (full
+// precision over 28 binades, whatever the scales), and the group's product is added to O in fp32
+// at its own scale. Q is f16 too, scaled by a power of two per row, exact for elements within
+// 2^-28 of the row's largest. (The e4m3 form of mma.sync, with Q and P in two parts each, measured
+// slower: 184 against 165 us on 32 ragged streams.)
 #include "kv_cache.cuh"
 #include "sm100.cuh"
-#include "tma_map.cuh"
 
 namespace bsa {
 namespace {
@@ -37,36 +37,28 @@ using namespace kv;
 using sm100::ex2_approx;
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32 + 32;           // and the producer's warp
+constexpr int kThreads = kWarps * 32;
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <bool FP8, int M>
 struct Cfg {
-    // e4m3: K, V, and their scales; bf16: K and V. Two blocks share an SM.
-    static constexpr uint32_t kV = FP8 ? 8192 : 16384;
-    static constexpr uint32_t kStage = FP8 ? 2 * 8192 + 2 * 128 : 2 * 16384;
-    // e4m3: even, so that a stage always belongs to the same half of the warps
-    static constexpr int NS = FP8 ? 4 : (M == 8 ? 3 : 2);
-    static constexpr int kSharers = FP8 ? 4 : 8;                      // warps that read a tile
-    static constexpr uint32_t kMerge = NS * kStage;                   // [warp][row][64 + 2]
-    static constexpr uint32_t kCtl = kMerge + kWarps * M * 66 * 4;
+    static constexpr int kKeys = FP8 ? 32 : 16;                       // keys of a group
+    static constexpr int kPer = kUnit / kKeys;                        // groups of a unit
+    static constexpr uint32_t kV = 2048;                              // a stage: K, V, K scales, V scales
+    static constexpr uint32_t kStage = 4096 + (FP8 ? 64 : 0);
+    static constexpr int kStages = 3;
+    static constexpr uint32_t kMerge = kWarps * kStages * kStage;     // [4][row][64], [4][row][2]
+    static constexpr uint32_t kSmem = kMerge + 4 * M * 66 * 4;
 };
 
-template <int M>
-struct Ctl {
-    uint64_t full[4], empty[4];
-    uint64_t rec_full[2], rec_empty[2], meet;
-    Rec rec[2];
-    int meta[4], tile[4];
-    uint32_t poison[M][2];                  // columns of a row that met a NaN or infinite value
-    int abort;
-    Start start;
-};
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort, status));
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
@@ -108,114 +100,119 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
 
 template <bool FP8, int M>
 __global__ void __launch_bounds__(kThreads, 2)
-kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-               const __grid_constant__ AttnArgs a) {
+kv_rows_kernel(const __grid_constant__ AttnArgs a) {
     using namespace sm100;
     using C = Cfg<FP8, M>;
     constexpr int NH = M / 8;               // 8-row halves in use
-    extern __shared__ __align__(1024) uint8_t smem[];
-    Ctl<M>& ctl = *reinterpret_cast<Ctl<M>*>(smem + C::kCtl);
+    constexpr int GK = C::kKeys;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ Start shared_start;
+    // columns of a row that met a NaN or infinite value; two sets, of which the next item's is
+    // written while the last one's is cleared
+    __shared__ uint32_t poisons[2][M][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int team = blockIdx.x;
-    volatile int* abort = &ctl.abort;
-
-    if (tid == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(&ctl.full[s], 1);
-            mbar_init(&ctl.empty[s], C::kSharers);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&ctl.rec_full[s], 1);
-            mbar_init(&ctl.rec_empty[s], kWarps);
-        }
-        mbar_init(&ctl.meet, kWarps);
-        ctl.abort = 0;
-        fence_mbar_init();
-    }
-    if (tid < M * 2) (&ctl.poison[0][0])[tid] = 0u;
+    if (tid < M * 4) (&poisons[0][0][0])[tid] = 0u;
     let_next_start();
     wait_for_previous();
-    // tile swizzles assume a 1024-byte aligned base; refuse to run otherwise
-    if ((smem_u32(smem) & 1023u) != 0u) {
-        if (tid == 0) {
-            record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
-            a.desc[team * kDesc] = 0;
-        }
-        return;
-    }
     int* tables = reinterpret_cast<int*>(smem);
-    const Start st = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &ctl.start);
+    const Start st = plan(a, team, tables, tables + BSA_KV_MAX_SEQS + 1, &shared_start);
     if (tid == 0) a.desc[team * kDesc] = 0;
     if (team >= st.teams || st.total == 0) return;
-    fence_async_shared();                   // the plan's tables lay where TMA writes next
     __syncthreads();
 
-    if (warp == kWarps) {
-        // ============================================================ producer
-        int U = 0, X = 0;
-        auto put_record = [&](const Rec& r) -> bool {
-            const int slot = X & 1;
-            if (X >= 2 && !warp_wait(&ctl.rec_empty[slot], ((X >> 1) - 1) & 1, abort, a.status)) return false;
-            if (lane == 0) {
-                ctl.rec[slot] = r;
-                mbar_arrive(&ctl.rec_full[slot]);
+    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+    float* mo = reinterpret_cast<float*>(smem + C::kMerge);           // [4][row][64]
+    float* mml = mo + 4 * M * 64;                                     // [4][row][2]
+    const int g = lane >> 2, t = lane & 3;
+
+    // first key of group x of a segment, and whether any row may see some of its keys
+    auto first_key = [](const Span& sp, int x) { return unit_of(sp, x / C::kPer) * kUnit + x % C::kPer * GK; };
+    auto wanted = [&](const Span& sp, int k0) { return k0 < sp.hi_max && (k0 + GK > sp.lo_min || k0 < a.sink); };
+    // this warp's groups of a segment are first_group, first_group + 8, ...
+    auto first_group = [&](const Walk& w) { return w.j0 * C::kPer + ((warp - w.j0 * C::kPer) & (kWarps - 1)); };
+
+    // ---------------------------------------------------------------- the loader
+    // lane i holds the pool rows of the group base + 8 i (its two 16-key halves) of its segment
+    Walk lw(a, st, team);
+    bool live = lw.next();
+    int lx = live ? first_group(lw) : 0, base = lx - 8 * 32, row0h = -1, row1h = -1;
+    uint32_t held = 0u;                     // bits 2 s, 2 s + 1: the halves of stage s hold keys
+    auto load_step = [&](int stage) {
+        while (live && lx >= lw.j1 * C::kPer) {
+            lw.done();
+            live = lw.next();
+            lx = live ? first_group(lw) : 0;
+            base = lx - 8 * 32;
+        }
+        uint32_t got = 0u;
+        if (live) {
+            if (lx - base >= 8 * 32) {
+                base = lx;
+                const int x = lx + 8 * lane, k0 = first_key(lw.span, x);
+                const bool in = x < lw.j1 * C::kPer && wanted(lw.span, k0);
+                const int32_t* pages = a.c.table + (long long)lw.s * a.c.max_pages;
+                auto row_of = [&](int k, bool use) {
+                    const int page = use ? pages[k >> a.c.pshift] : -1;
+                    if (page >= a.c.pages) record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
+                    return page < 0 || page >= a.c.pages
+                               ? -1
+                               : ((page * a.c.kv_heads + lw.h) << a.c.pshift) + (k & ((1 << a.c.pshift) - 1));
+                };
+                row0h = row_of(k0, in);
+                // pages of 16 tokens end inside a group of 32; the second one may lie past the tables
+                if (GK == 32)
+                    row1h = a.c.pshift > 4 ? (row0h < 0 ? -1 : row0h + 16) : row_of(k0 + 16, in && k0 + 16 < lw.span.hi_max);
             }
-            ++X;
-            return true;
-        };
-        auto begin = [](const Walk&, int) { return true; };
-        auto put_tile = [&](int meta, int t, int page, long long row, unsigned have, int at, int box) -> bool {
-            const int s = U % C::NS;
-            if (U >= C::NS && !warp_wait(&ctl.empty[s], ((U / C::NS) - 1) & 1, abort, a.status)) return false;
-            uint8_t* dst = smem + s * C::kStage;
-            if (lane == 0) {
-                ctl.meta[s] = meta;
-                ctl.tile[s] = t;
-                mbar_arrive_expect_tx(&ctl.full[s], __popc(have) * box * (FP8 ? 130 : 256));
-            }
-            __syncwarp();
-            if (page >= 0) {
-                if (FP8) {
-                    bulk_load(dst + at * 64, static_cast<const uint8_t*>(a.k) + row * 64, box * 64, &ctl.full[s]);
-                    bulk_load(dst + C::kV + at * 64, static_cast<const uint8_t*>(a.v) + row * 64, box * 64, &ctl.full[s]);
-                    bulk_load(dst + 16384 + at, a.ks + row, box, &ctl.full[s]);
-                    bulk_load(dst + 16384 + 128 + at, a.vs + row, box, &ctl.full[s]);
-                } else {
-                    tma_load_2d(dst + at * 128, &tm_k, &ctl.full[s], 0, (int)row);
-                    tma_load_2d(dst + C::kV + at * 128, &tm_v, &ctl.full[s], 0, (int)row);
+            const int from = (lx - base) >> 3;
+            const int r0h = __shfl_sync(0xffffffffu, row0h, from);
+            const int r1h = GK == 32 ? __shfl_sync(0xffffffffu, row1h, from) : -1;
+            got = (r0h >= 0 ? 1u : 0u) | (r1h >= 0 ? 2u : 0u);
+            const uint32_t dst = ring + stage * C::kStage;
+            if (!FP8) {
+                if (got) {
+                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + (long long)r0h * 128 + lane * 16;
+                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + (long long)r0h * 128 + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 4 + (lane >> 3);
+                        const uint32_t to = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                        cp16(to, kp + i * 512);
+                        cp16(to + C::kV, vp + i * 512);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = half ? r1h : r0h;
+                    if (row < 0) continue;
+                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + (long long)row * 64 + lane * 16;
+                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + (long long)row * 64 + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        cp16(dst + half * 1024 + i * 512 + lane * 16, kp + i * 512);
+                        cp16(dst + C::kV + half * 1024 + i * 512 + lane * 16, vp + i * 512);
+                    }
+                    if (lane < 2) cp16(dst + 4096 + lane * 32 + half * 16, (lane ? a.vs : a.ks) + row);
                 }
             }
-            ++U;
-            return true;
-        };
-        if (produce(a, st, team, 0, lane, put_record, begin, put_tile)) {
-            Rec rec = {};
-            rec.tiles = -1;
-            put_record(rec);
+            lx += 8;
         }
-        // every copy has landed before the block's shared memory goes away
-        volatile int never = 0;
-        for (int u = max(0, U - C::NS); u < U; ++u)
-            mbar_wait(&ctl.full[u % C::NS], (u / C::NS) & 1, &never, a.status, 50000000ull);
-        return;
-    }
-
-    // ================================================================ arithmetic
-    float* mo = reinterpret_cast<float*>(smem + C::kMerge);           // [warp][row][64]
-    float* mml = mo + kWarps * M * 64;                                // [warp][row][2]
-    const int g = lane >> 2, t = lane & 3;
-    int U = 0, met = 0;
-    auto meet = [&]() -> bool {             // the eight warps; bounded like every wait
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.meet);
-        return warp_wait(&ctl.meet, met++ & 1, abort, a.status);
+        held = (held & ~(3u << (2 * stage))) | (got << (2 * stage));
+        cp_commit();
     };
-    for (int X = 0;; ++X) {
-        if (!warp_wait(&ctl.rec_full[X & 1], (X >> 1) & 1, abort, a.status)) break;
-        const Rec& rec = ctl.rec[X & 1];
-        const int tiles = rec.tiles;
-        if (tiles < 0) break;
-        const int nrows = rec.nrows, r0 = rec.r0, row0 = rec.row0, pos0 = rec.pos0, len = rec.len;
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) load_step(i);
+
+    // ---------------------------------------------------------------- arithmetic
+    int stage = 0, set = 0;
+    Walk w(a, st, team);
+    for (; w.next(); w.done(), set ^= 1) {
+        uint32_t(&poison)[M][2] = poisons[set];
+        const int row0 = w.q.row0, pos0 = w.q.len - w.q.n, len = w.q.len;
+        const int r0 = w.rg * M;            // R = 1, mr = M
+        const int nrows = min(M, w.q.n * a.group - r0);
+        const Span& sp = w.span;
         // ---------------------------------------------------------------- Q
         // k-step ks takes the words qf[ks][hh] and qf[ks][NH + hh] of rows 8 hh + g
         uint32_t qf[4][2 * NH];
@@ -227,7 +224,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (r < nrows) {
                 const int i = a.by_group.of(r0 + r);
                 const __nv_bfloat16* p =
-                    a.q + (long long)(row0 + i) * a.q_stride + ((long long)rec.h * a.group + (r0 + r - i * a.group)) * 64;
+                    a.q + (long long)(row0 + i) * a.q_stride + ((long long)w.h * a.group + (r0 + r - i * a.group)) * 64;
                 const uint4* p4 = reinterpret_cast<const uint4*>(p);
                 c0 = p4[2 * t];
                 c1 = p4[2 * t + 1];
@@ -267,28 +264,25 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
 
         if constexpr (!FP8) {
-        for (int u = 0; u < tiles; ++u, ++U) {
-            const int s = U % C::NS;
-            if (!warp_wait(&ctl.full[s], (U / C::NS) & 1, abort, a.status)) return;
-            const int meta = ctl.meta[s], kb = ctl.tile[s] * kUnit + warp * 16;
-            const bool want = ((meta >> warp) & 1) &&
-                              ((meta & kFull) || (kb < rec.hi_max && (kb + 16 > rec.lo_min || kb < a.sink)));
-            const bool all = (meta & kFull) || (kb + 16 <= rec.hi_min &&
-                                                (kb >= rec.lo_max || kb + 16 <= min(a.sink, rec.lo_min)));
-            if (!want) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.empty[s]);
-                continue;
-            }
+        for (int gx = first_group(w); gx < w.j1 * C::kPer; gx += 8) {
+            cp_wait<C::kStages - 2>();
+            __syncwarp();
+            const uint32_t there = (held >> (2 * stage)) & 3u;
+            const uint32_t src = ring + stage * C::kStage;
+            const int next_stage = stage == 0 ? C::kStages - 1 : stage - 1;   // emptied by the step before
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+            load_step(next_stage);
+            if (there == 0u) continue;
+            const int kb = first_key(sp, gx);
+            const bool all = kb + 16 <= sp.hi_min && (kb >= sp.lo_max || kb + 16 <= min(a.sink, sp.lo_min));
             // column x (0 .. 7) of the scores' half jj stands for key jj * 8 + x of the warp's 16
-            const uint32_t src = smem_u32(smem + s * C::kStage);
             // ------------------------------------------------------------ scores
             float x[2][4];
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) x[jj][c] = 0.f;
-                const int r = warp * 16 + jj * 8 + g;
+                const int r = jj * 8 + g;
                 const uint4 k0 = lds16(src + r * 128 + (((2 * t) ^ (r & 7)) << 4));
                 const uint4 k1 = lds16(src + r * 128 + (((2 * t + 1) ^ (r & 7)) << 4));
                 const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
@@ -303,15 +297,13 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             uint32_t vw[4][4];              // 8 values of the lane's four keys
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = warp * 16 + (i >> 1) * 8 + 2 * t + (i & 1);
+                const int r = (i >> 1) * 8 + 2 * t + (i & 1);
                 const uint4 v = lds16(src + C::kV + r * 128 + ((g ^ (r & 7)) << 4));
                 vw[i][0] = v.x;
                 vw[i][1] = v.y;
                 vw[i][2] = v.z;
                 vw[i][3] = v.w;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.empty[s]);
             uint32_t seen = 0xffu;          // bit (jj * 4 + c): x[jj][c] counts
             if (!all) {
                 seen = 0u;
@@ -353,7 +345,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             int lo, hi;
                             visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
                             if (key < hi && (key >= lo || key < a.sink))
-                                atomicOr(&ctl.poison[r][g >> 2], cols << ((g & 3) * 8));
+                                atomicOr(&poison[r][g >> 2], cols << ((g & 3) * 8));
                         }
                     }
                 }
@@ -409,31 +401,26 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
         }
         } else {
-        for (int u = 0; u < tiles; ++u, ++U) {
-            if ((U & 1) != warp >> 2) continue;   // the other half's tile
-            const int s = U % C::NS, sub = warp & 3;
-            if (!warp_wait(&ctl.full[s], (U / C::NS) & 1, abort, a.status)) return;
-            const int meta = ctl.meta[s], kb = ctl.tile[s] * kUnit + sub * 32;
-            const int there = (meta >> (2 * sub)) & 3;   // pages of the two 16-key halves
-            const bool want = there != 0 &&
-                              ((meta & kFull) || (kb < rec.hi_max && (kb + 32 > rec.lo_min || kb < a.sink)));
-            const bool all = (meta & kFull) || (there == 3 && kb + 32 <= rec.hi_min &&
-                                                (kb >= rec.lo_max || kb + 32 <= min(a.sink, rec.lo_min)));
-            if (!want) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.empty[s]);
-                continue;
-            }
+        for (int gx = first_group(w); gx < w.j1 * C::kPer; gx += 8) {
+            cp_wait<C::kStages - 2>();
+            __syncwarp();
+            const uint32_t there = (held >> (2 * stage)) & 3u;
+            const uint32_t src = ring + stage * C::kStage;
+            const int next_stage = stage == 0 ? C::kStages - 1 : stage - 1;   // emptied by the step before
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+            load_step(next_stage);
+            if (there == 0u) continue;
+            const int kb = first_key(sp, gx);
+            const bool all = there == 3u && kb + 32 <= sp.hi_min && (kb >= sp.lo_max || kb + 32 <= min(a.sink, sp.lo_min));
             // column c of the scores' eighth n stands for key 8 n + c / 2 (c even), 8 n + 4 + (c / 2 ^ 1)
             // (odd): pairs of columns differ in parity and equal columns of a quad lie together
-            const uint32_t src = smem_u32(smem + s * C::kStage);
             const int kg = g & 1 ? 4 + ((g >> 1) ^ 1) : g >> 1;   // key of column g
             const int k1 = 4 + (t ^ 1);                           // key of column 2 t + 1; 2 t: t
             // ------------------------------------------------------------ scores
             float x[4][2 * NH];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const uint4 kw = lds16(src + (sub * 32 + 8 * n + kg) * 64 + t * 16);
+                const uint4 kw = lds16(src + (8 * n + kg) * 64 + t * 16);
                 const uint32_t kc[4] = {kw.x, kw.y, kw.z, kw.w};
                 float h[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -448,8 +435,8 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float ve[4][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const uint4 kb4 = lds16(src + 16384 + sub * 32 + half * 16);
-                const uint4 vb4 = lds16(src + 16384 + 128 + sub * 32 + half * 16);
+                const uint4 kb4 = lds16(src + 4096 + half * 16);
+                const uint4 vb4 = lds16(src + 4096 + 32 + half * 16);
                 const uint32_t kw[4] = {kb4.x, kb4.y, kb4.z, kb4.w}, vw[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -472,9 +459,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    vc[half][i] = lds8(src + C::kV + (sub * 32 + half * 16 + (i >> 1) * 8 + (i & 1 ? k1 : t)) * 64 + g * 8);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.empty[s]);
+                    vc[half][i] = lds8(src + C::kV + (half * 16 + (i >> 1) * 8 + (i & 1 ? k1 : t)) * 64 + g * 8);
             // ------------------------------------------------------------ what is seen
             if (!all) {
 #pragma unroll
@@ -593,34 +578,69 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
 
         // -------------------------------------------------------------------- the block's warps
+        // warps 4 .. 7 hand theirs to warps 0 .. 3, those the sums to the whole block. Lane (g, t)
+        // holds columns 16 t .. 16 t + 15 of row g: o[j][0] is 16 t + j, o[j][1] 8 further
+        auto place = [&](int r, int c, int j8) {
+            return reinterpret_cast<float4*>(mo + ((warp & 3) * M + r) * 64 + 16 * t + 8 * c + j8);
+        };
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
             l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
             l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-            const int r = warp * M + hh * 8 + g;
-            // lane (g, t) holds columns 16 t .. 16 t + 15 of row g: o[j][0] is 16 t + j, o[j][1] 8 further
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int j8 = 0; j8 < 8; j8 += 4)
-                    *reinterpret_cast<float4*>(mo + r * 64 + 16 * t + 8 * c + j8) =
-                        make_float4(o[j8][2 * hh + c], o[j8 + 1][2 * hh + c], o[j8 + 2][2 * hh + c], o[j8 + 3][2 * hh + c]);
-            if (t == 0) {
-                mml[r * 2] = m[hh];
-                mml[r * 2 + 1] = l[hh];
-            }
         }
-        if (!meet()) return;
-        const bool whole = rec.whole;
-        float* part = part_at<M>(a, team, rec.run, 0);
+        auto put = [&] {
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                const int r = hh * 8 + g;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j8 = 0; j8 < 8; j8 += 4)
+                        *place(r, c, j8) = make_float4(o[j8][2 * hh + c], o[j8 + 1][2 * hh + c], o[j8 + 2][2 * hh + c],
+                                                       o[j8 + 3][2 * hh + c]);
+                if (t == 0) {
+                    mml[((warp & 3) * M + r) * 2] = m[hh];
+                    mml[((warp & 3) * M + r) * 2 + 1] = l[hh];
+                }
+            }
+        };
+        if (warp >= 4) put();
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                const int r = hh * 8 + g;
+                const float mk = mml[(warp * M + r) * 2], lk = mml[(warp * M + r) * 2 + 1];
+                const float n = fmaxf(m[hh], mk);
+                const float f0 = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
+                const float f1 = mk == -INFINITY ? 0.f : ex2_approx(mk - n);
+                m[hh] = n;
+                l[hh] = l[hh] * f0 + lk * f1;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j8 = 0; j8 < 8; j8 += 4) {
+                        const float4 v = *place(r, c, j8);
+                        o[j8][2 * hh + c] = o[j8][2 * hh + c] * f0 + v.x * f1;
+                        o[j8 + 1][2 * hh + c] = o[j8 + 1][2 * hh + c] * f0 + v.y * f1;
+                        o[j8 + 2][2 * hh + c] = o[j8 + 2][2 * hh + c] * f0 + v.z * f1;
+                        o[j8 + 3][2 * hh + c] = o[j8 + 3][2 * hh + c] * f0 + v.w * f1;
+                    }
+            }
+            __syncwarp();
+            put();
+        }
+        __syncthreads();
+        const bool whole = w.has_start && w.has_end;
+        float* part = part_at<M>(a, team, w.has_start ? 1 : 0, 0);
         if (tid < M * 16) {
             const int r = tid >> 4, c4 = (tid & 15) * 4;
             float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, mml[(k * M + r) * 2]);
+            for (int k = 0; k < 4; ++k) mm = fmaxf(mm, mml[(k * M + r) * 2]);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const float mk = mml[(k * M + r) * 2];
                 const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - mm);
                 const float4 v = *reinterpret_cast<const float4*>(mo + (k * M + r) * 64 + c4);
@@ -632,7 +652,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             }
             // l = 0: nothing seen. NaN stays.
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            const uint32_t bad = ctl.poison[r][c4 >> 5] >> (c4 & 31);
+            const uint32_t bad = poison[r][c4 >> 5] >> (c4 & 31);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 acc[k] *= inv;
@@ -642,7 +662,7 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (r < nrows) {
                 if (whole) {
                     const int i = a.by_group.of(r0 + r);
-                    const int head = rec.h * a.group + (r0 + r - i * a.group);
+                    const int head = w.h * a.group + (r0 + r - i * a.group);
                     *reinterpret_cast<uint2*>(a.out + (long long)(row0 + i) * a.out_stride + head * 64 + c4) =
                         make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
                     if (c4 == 0 && a.lse != nullptr) a.lse[(long long)head * a.rows + row0 + i] = lse;
@@ -652,10 +672,19 @@ kv_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 }
             }
         }
-        if (!meet()) return;
-        if (tid < M * 2) (&ctl.poison[0][0])[tid] = 0u;
-        if (lane == 0) mbar_arrive(&ctl.rec_empty[X & 1]);
+        if (tid == 0 && !whole && w.has_start) {   // the merge kernel's record of this item
+            int* d = a.desc + team * kDesc;
+            d[1] = row0;
+            d[2] = w.q.n;
+            d[3] = w.h;
+            d[4] = w.rg;
+            d[5] = st.team_of(w.item + max(1, sp.count) - 1);
+            d[0] = 1;
+        }
+        __syncthreads();
+        if (tid < M * 2) (&poison[0][0])[tid] = 0u;
     }
+    cp_wait<0>();
 }
 
 // Joins the partial results of an item that crosses team ends: the team that holds its first
@@ -739,15 +768,9 @@ template <bool FP8, int M>
 cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
     using C = Cfg<FP8, M>;
     auto kern = kv_rows_kernel<FP8, M>;
-    const size_t smem = C::kCtl + sizeof(Ctl<M>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    CUtensorMap k = {}, v = {};
-    const uint64_t rows = ((uint64_t)a.c.pages * a.c.kv_heads) << a.c.pshift;
-    const uint32_t box = a.c.pshift < 7 ? 1u << a.c.pshift : 128u;
-    if (!FP8 && (!make_tile_map(&k, a.k, rows, 64, box, false) || !make_tile_map(&v, a.v, rows, 64, box, false)))
-        return cudaErrorInvalidValue;
-    return launch_early(kern, dim3(a.max_teams), kThreads, smem, st, k, v, a);
+    return launch_early(kern, dim3(a.max_teams), kThreads, C::kSmem, st, a);
 }
 
 }  // namespace

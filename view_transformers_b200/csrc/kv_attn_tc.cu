@@ -184,7 +184,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 q_loads = ++I;
                 return true;
             };
-            auto put_tile = [&](int meta, int t, int page, long long row, unsigned have, int at, int box) -> bool {
+            auto put_tile = [&](int meta, int t, int boxes, int rows, int at) -> bool {
+                const int box = kUnit / boxes, i = lane - at;   // this lane's box
+                const int row = i >= 0 && i < boxes ? rows : -1, k = i * box;
+                const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
                 if (!FP8) {
                     const int st = U % NS;
                     if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) return false;
@@ -194,9 +197,9 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         mbar_arrive_expect_tx(&ctl.k_full[st], __popc(have) * box * 256);
                     }
                     __syncwarp();
-                    if (page >= 0) {
-                        tma_load_2d(smem + C::kOffK + st * kTile + at * 128, &tm_k, &ctl.k_full[st], 0, (int)row);
-                        tma_load_2d(smem + C::kOffV + st * kTile + at * 128, &tm_v, &ctl.k_full[st], 0, (int)row);
+                    if (row >= 0) {
+                        tma_load_2d(smem + C::kOffK + st * kTile + k * 128, &tm_k, &ctl.k_full[st], 0, row);
+                        tma_load_2d(smem + C::kOffV + st * kTile + k * 128, &tm_v, &ctl.k_full[st], 0, row);
                     }
                     issued = U + 1;
                 } else {
@@ -212,10 +215,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             mbar_arrive_expect_tx(&ctl.raw_full[slot], __popc(have) * box * 65);
                         }
                         __syncwarp();
-                        if (page >= 0) {
-                            bulk_load(dst + at * 64, static_cast<const uint8_t*>(half ? a.v : a.k) + row * 64, box * 64,
-                                      &ctl.raw_full[slot]);
-                            bulk_load(dst + 8192 + at, (half ? a.vs : a.ks) + row, box, &ctl.raw_full[slot]);
+                        if (row >= 0) {
+                            bulk_load(dst + k * 64, static_cast<const uint8_t*>(half ? a.v : a.k) + (long long)row * 64,
+                                      box * 64, &ctl.raw_full[slot]);
+                            bulk_load(dst + 8192 + k, (half ? a.vs : a.ks) + row, box, &ctl.raw_full[slot]);
                         }
                         issued = x + 1;
                     }

@@ -397,10 +397,11 @@ struct Rec {
 enum { kFull = 0x100, kFirst = 0x200, kLast = 0x400, kEnd = 0x800 };
 
 // The producer's part of a block, run by one warp: walks the team's segments, hands out a record
-// for each (put_record), announces those with key tiles (begin) and then hands out their tiles
-// (put_tile), one box of up to 128 keys of a page per lane: `page` (negative: none), `row`, its
-// first row in the pools, `at`, the box's first key within the tile, and the lanes that have one. Any of
-// the three returns false to stop. True when all is handed out.
+// for each (put_record), announces those with key tiles (begin) and then hands out their tiles:
+// put_tile(meta, t, boxes, rows, at) gets tile t's words and, in lanes at .. at + boxes - 1 of
+// `rows`, the first pool rows of its boxes (up to 128 keys of a page each; negative: no page). Any
+// of the three returns false to stop. True when all is handed out. What can be computed for 32
+// boxes at once is: the warp shares its scheduler with the arithmetic.
 template <class PutRecord, class Begin, class PutTile>
 __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, int team, int member, int lane,
                                         PutRecord put_record, Begin begin, PutTile put_tile) {
@@ -435,42 +436,44 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
         rec.hi_min = own.hi_min;
         if (!put_record(rec)) return false;
         if (tiles > 0 && !begin(w, r0)) return false;
-        // page ids come 32 boxes at a time, the next ones while these are handed out: lane i holds
-        // box i % boxes of the run's tile jb + i / boxes
-        const int boxes = kUnit >> shift, per = 32 / boxes;
+        // lane i: box i % boxes of the run's tile jb + i / boxes; the next batch's page ids are on
+        // their way while this one's tiles are handed out
+        const int bshift = 7 - shift, boxes = 1 << bshift, per = 32 >> bshift;
+        const int sub = (lane & (boxes - 1)) * box;
+        const int32_t* pages = a.c.table + (long long)w.s * a.c.max_pages;
         auto fetch = [&](int jb) {
-            const int j = jb + (lane >> (7 - shift));
-            const int k0 = unit_of(w.span, j) * kUnit + (lane & (boxes - 1)) * box;
-            return j < w.j1 && wanted(k0, box) ? a.c.table[(long long)w.s * a.c.max_pages + (k0 >> a.c.pshift)] : -1;
+            const int j = jb + (lane >> bshift), k0 = unit_of(w.span, j) * kUnit + sub;
+            return j < w.j1 && wanted(k0, box) ? pages[k0 >> a.c.pshift] : -1;
         };
-        int ids = fetch(w.j0), ahead = fetch(w.j0 + per), jb = w.j0;
-        int left = tiles;
-        for (int j = w.j0; left > 0 && j < w.j1; ++j) {
-            if (j - jb == per) {
-                jb = j;
-                ids = ahead;
-                ahead = fetch(j + per);
-            }
-            const int t = unit_of(w.span, j), key = t * kUnit;
-            if (!wanted(key, kUnit)) continue;
-            const int k0 = key + lane * box;
-            int page = __shfl_sync(0xffffffffu, ids, (j - jb) * boxes + (lane & (boxes - 1)));
-            if (lane >= boxes) page = -1;
+        int ahead = fetch(w.j0), left = tiles;
+        for (int jb = w.j0; left > 0 && jb < w.j1; jb += per) {
+            int page = ahead;
+            ahead = fetch(jb + per);
+            const int j = jb + (lane >> bshift), mine = unit_of(w.span, j), key = mine * kUnit;
             if (page >= a.c.pages) {
                 record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
                 page = -1;
             }
+            const int rows = page < 0 ? -1
+                : ((page * a.c.kv_heads + w.h) << a.c.pshift) + ((key + sub) & ((1 << a.c.pshift) - 1));
             const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
-            int meta = (left == tiles ? kFirst : 0) | (left == 1 ? kLast : 0);
-            --left;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) meta |= ((have >> ((i * 16) >> shift)) & 1u) << i;
-            if ((meta & 0xff) == 0xff && key + kUnit <= own.hi_min &&
-                (key >= own.lo_max || key + kUnit <= min(a.sink, own.lo_min)))
-                meta |= kFull;
-            const long long row = page < 0 ? 0
-                : (((long long)page * a.c.kv_heads + w.h) << a.c.pshift) + (k0 & ((1 << a.c.pshift) - 1));
-            if (!put_tile(meta, t, page, row, have, lane * box, box)) return false;
+            const unsigned want = __ballot_sync(0xffffffffu, j < w.j1 && wanted(key, kUnit));
+            const unsigned whole = __ballot_sync(0xffffffffu, key + kUnit <= own.hi_min &&
+                                                                  (key >= own.lo_max || key + kUnit <= min(a.sink, own.lo_min)));
+            for (int at = 0; at < 32 && left > 0; at += boxes) {
+                if (!((want >> at) & 1u)) continue;
+                const unsigned got = (have >> at) & ((1u << boxes) - 1u);
+                int meta = 0xff;
+                if (got != (1u << boxes) - 1u) {
+                    meta = 0;
+                    for (int i = 0; i < 8; ++i) meta |= ((got >> ((i * 16) >> shift)) & 1u) << i;
+                } else if ((whole >> at) & 1u) {
+                    meta |= kFull;
+                }
+                meta |= (left == tiles ? kFirst : 0) | (left == 1 ? kLast : 0);
+                --left;
+                if (!put_tile(meta, __shfl_sync(0xffffffffu, mine, at), boxes, rows, at)) return false;
+            }
         }
         if (lane == 0 && member == 0 && !rec.whole && w.has_start) {   // the merge kernel's record of this item
             int* d = a.desc + team * kDesc;
