@@ -94,6 +94,13 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {
     return r;
 }
 
+// the scales whose bytes `pick` takes from two words of scale bytes
+__device__ __forceinline__ float2 scales_of(uint32_t w0, uint32_t w1, uint32_t pick) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, lo;\n\t}" : "=r"(r) : "r"(__byte_perm(w0, w1, pick)));
+    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+
 __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -132,12 +139,16 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
     // this warp's groups of a segment are first_group, first_group + 8, ...
     auto first_group = [&](const Walk& w) { return w.j0 * C::kPer + ((warp - w.j0 * C::kPer) & (kWarps - 1)); };
 
+    Walk w(a, st, team);
+    bool more = w.next();
     // ---------------------------------------------------------------- the loader
-    // lane i holds the pool rows of the group base + 8 i (its two 16-key halves) of its segment
-    Walk lw(a, st, team);
-    bool live = lw.next();
+    // lane i holds the pool rows of the group base + 8 i (its two 16-key halves) of its segment, and
+    // bit i of `full` tells whether every row sees every key of that group
+    Walk lw = w;
+    bool live = more;
     int lx = live ? first_group(lw) : 0, base = lx - 8 * 32, row0h = -1, row1h = -1;
-    uint32_t held = 0u;                     // bits 2 s, 2 s + 1: the halves of stage s hold keys
+    uint32_t full = 0u;
+    uint32_t held = 0u;                     // 4 bits per stage: the halves that hold keys; full
     auto load_step = [&](int stage) {
         while (live && lx >= lw.j1 * C::kPer) {
             lw.done();
@@ -149,8 +160,9 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
         if (live) {
             if (lx - base >= 8 * 32) {
                 base = lx;
-                const int x = lx + 8 * lane, k0 = first_key(lw.span, x);
-                const bool in = x < lw.j1 * C::kPer && wanted(lw.span, k0);
+                const Span& sp = lw.span;
+                const int x = lx + 8 * lane, k0 = first_key(sp, x);
+                const bool in = x < lw.j1 * C::kPer && wanted(sp, k0);
                 const int32_t* pages = a.c.table + (long long)lw.s * a.c.max_pages;
                 auto row_of = [&](int k, bool use) {
                     const int page = use ? pages[k >> a.c.pshift] : -1;
@@ -162,56 +174,64 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                 row0h = row_of(k0, in);
                 // pages of 16 tokens end inside a group of 32; the second one may lie past the tables
                 if (GK == 32)
-                    row1h = a.c.pshift > 4 ? (row0h < 0 ? -1 : row0h + 16) : row_of(k0 + 16, in && k0 + 16 < lw.span.hi_max);
+                    row1h = a.c.pshift > 4 ? (row0h < 0 ? -1 : row0h + 16) : row_of(k0 + 16, in && k0 + 16 < sp.hi_max);
+                full = __ballot_sync(0xffffffffu, row0h >= 0 && (GK == 16 || row1h >= 0) && k0 + GK <= sp.hi_min &&
+                                                      (k0 >= sp.lo_max || k0 + GK <= min(a.sink, sp.lo_min)));
             }
             const int from = (lx - base) >> 3;
             const int r0h = __shfl_sync(0xffffffffu, row0h, from);
             const int r1h = GK == 32 ? __shfl_sync(0xffffffffu, row1h, from) : -1;
-            got = (r0h >= 0 ? 1u : 0u) | (r1h >= 0 ? 2u : 0u);
-            const uint32_t dst = ring + stage * C::kStage;
+            got = (r0h >= 0 ? 1u : 0u) | (r1h >= 0 ? 2u : 0u) | ((full >> from) & 1u) << 2;
+            const uint32_t dst = ring + stage * C::kStage + lane * 16;
             if (!FP8) {
                 if (got) {
-                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + (long long)r0h * 128 + lane * 16;
-                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + (long long)r0h * 128 + lane * 16;
+                    const long long at = (long long)r0h * 128 + lane * 16;
+                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + at;
+                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + at;
+                    // rows 4 i + lane / 8: the swizzle has one of two values
+                    const int c = lane & 7, r = lane >> 3;
+                    const uint32_t even = dst + ((c ^ r) - c) * 16, odd = dst + ((c ^ (r + 4)) - c) * 16;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = i * 4 + (lane >> 3);
-                        const uint32_t to = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                        cp16(to, kp + i * 512);
-                        cp16(to + C::kV, vp + i * 512);
+                        cp16((i & 1 ? odd : even) + i * 512, kp + i * 512);
+                        cp16((i & 1 ? odd : even) + i * 512 + C::kV, vp + i * 512);
                     }
                 }
             } else {
+                auto copy = [&](int row, uint32_t to, int n) {   // n times 8 rows of K and V
+                    const long long at = (long long)row * 64 + lane * 16;
+                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + at;
+                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + at;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int row = half ? r1h : r0h;
-                    if (row < 0) continue;
-                    const uint8_t* kp = static_cast<const uint8_t*>(a.k) + (long long)row * 64 + lane * 16;
-                    const uint8_t* vp = static_cast<const uint8_t*>(a.v) + (long long)row * 64 + lane * 16;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        cp16(dst + half * 1024 + i * 512 + lane * 16, kp + i * 512);
-                        cp16(dst + C::kV + half * 1024 + i * 512 + lane * 16, vp + i * 512);
+                    for (int i = 0; i < n; ++i) {
+                        cp16(to + i * 512, kp + i * 512);
+                        cp16(to + i * 512 + C::kV, vp + i * 512);
                     }
-                    if (lane < 2) cp16(dst + 4096 + lane * 32 + half * 16, (lane ? a.vs : a.ks) + row);
+                };
+                const uint8_t* sc = lane & 2 ? a.vs : a.ks;      // lanes 0, 1: K, 2, 3: V; the halves
+                if ((got & 3u) == 3u && r1h == r0h + 16) {
+                    copy(r0h, dst, 4);
+                    if (lane < 4) cp16(dst + 4096, sc + r0h + (lane & 1) * 16);
+                } else {
+                    if (r0h >= 0) copy(r0h, dst, 2);
+                    if (r1h >= 0) copy(r1h, dst + 1024, 2);
+                    const int rs = lane & 1 ? r1h : r0h;
+                    if (lane < 4 && rs >= 0) cp16(dst + 4096, sc + rs);
                 }
             }
             lx += 8;
         }
-        held = (held & ~(3u << (2 * stage))) | (got << (2 * stage));
+        held = (held & ~(15u << (4 * stage))) | (got << (4 * stage));
         cp_commit();
     };
+    // ---------------------------------------------------------------- arithmetic
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load_step(i);
-
-    // ---------------------------------------------------------------- arithmetic
     int stage = 0, set = 0;
-    Walk w(a, st, team);
-    for (; w.next(); w.done(), set ^= 1) {
+    for (; more; set ^= 1) {
         uint32_t(&poison)[M][2] = poisons[set];
         const int row0 = w.q.row0, pos0 = w.q.len - w.q.n, len = w.q.len;
-        const int r0 = w.rg * M;            // R = 1, mr = M
-        const int nrows = min(M, w.q.n * a.group - r0);
+        const int r0 = w.rg * M, nrows = min(M, w.q.n * a.group - r0);
         const Span& sp = w.span;
         // ---------------------------------------------------------------- Q
         // k-step ks takes the words qf[ks][hh] and qf[ks][NH + hh] of rows 8 hh + g
@@ -223,11 +243,10 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
             uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
             if (r < nrows) {
                 const int i = a.by_group.of(r0 + r);
-                const __nv_bfloat16* p =
-                    a.q + (long long)(row0 + i) * a.q_stride + ((long long)w.h * a.group + (r0 + r - i * a.group)) * 64;
-                const uint4* p4 = reinterpret_cast<const uint4*>(p);
-                c0 = p4[2 * t];
-                c1 = p4[2 * t + 1];
+                const uint4* p = reinterpret_cast<const uint4*>(a.q + (long long)(row0 + i) * a.q_stride +
+                                                                ((long long)w.h * a.group + (r0 + r - i * a.group)) * 64);
+                c0 = p[2 * t];
+                c1 = p[2 * t + 1];
             }
             uint32_t wds[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
             rowf[hh] = kScaleLog2;
@@ -264,17 +283,18 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
         }
 
         if constexpr (!FP8) {
+#pragma unroll 1
         for (int gx = first_group(w); gx < w.j1 * C::kPer; gx += 8) {
             cp_wait<C::kStages - 2>();
             __syncwarp();
-            const uint32_t there = (held >> (2 * stage)) & 3u;
+            const uint32_t there = (held >> (4 * stage)) & 3u;
+            const bool all = (held >> (4 * stage)) & 4u;
             const uint32_t src = ring + stage * C::kStage;
             const int next_stage = stage == 0 ? C::kStages - 1 : stage - 1;   // emptied by the step before
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
             load_step(next_stage);
             if (there == 0u) continue;
-            const int kb = first_key(sp, gx);
-            const bool all = kb + 16 <= sp.hi_min && (kb >= sp.lo_max || kb + 16 <= min(a.sink, sp.lo_min));
+            const int kb = all ? 0 : first_key(sp, gx);
             // column x (0 .. 7) of the scores' half jj stands for key jj * 8 + x of the warp's 16
             // ------------------------------------------------------------ scores
             float x[2][4];
@@ -401,21 +421,23 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
             }
         }
         } else {
+#pragma unroll 1
         for (int gx = first_group(w); gx < w.j1 * C::kPer; gx += 8) {
             cp_wait<C::kStages - 2>();
             __syncwarp();
-            const uint32_t there = (held >> (2 * stage)) & 3u;
+            const uint32_t there = (held >> (4 * stage)) & 3u;
+            const bool all = (held >> (4 * stage)) & 4u;
             const uint32_t src = ring + stage * C::kStage;
             const int next_stage = stage == 0 ? C::kStages - 1 : stage - 1;   // emptied by the step before
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
             load_step(next_stage);
             if (there == 0u) continue;
-            const int kb = first_key(sp, gx);
-            const bool all = there == 3u && kb + 32 <= sp.hi_min && (kb >= sp.lo_max || kb + 32 <= min(a.sink, sp.lo_min));
+            const int kb = all ? 0 : first_key(sp, gx);
             // column c of the scores' eighth n stands for key 8 n + c / 2 (c even), 8 n + 4 + (c / 2 ^ 1)
             // (odd): pairs of columns differ in parity and equal columns of a quad lie together
             const int kg = g & 1 ? 4 + ((g >> 1) ^ 1) : g >> 1;   // key of column g
             const int k1 = 4 + (t ^ 1);                           // key of column 2 t + 1; 2 t: t
+            const uint32_t pick = t | k1 << 4;                    // their bytes of two words
             // ------------------------------------------------------------ scores
             float x[4][2 * NH];
 #pragma unroll
@@ -430,26 +452,23 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                 for (int c = 0; c < 2 * NH; ++c) x[n][c] = h[c];
             }
-            // scales: x takes the K row's as a factor (byte 255 gives inf, and inf - inf makes the score
-            // NaN), y = x + the V row's exponent
-            float ve[4][2];
+            // the rows' scales (NaN for byte 255): a K row's goes into the scores, a V row's into P
+            float vs[4][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint4 kb4 = lds16(src + 4096 + half * 16);
                 const uint4 vb4 = lds16(src + 4096 + 32 + half * 16);
-                const uint32_t kw[4] = {kb4.x, kb4.y, kb4.z, kb4.w}, vw[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int n = 2 * half + i;
+                    const float2 ks = scales_of(i ? kb4.z : kb4.x, i ? kb4.w : kb4.y, pick);
+                    const float2 v = scales_of(i ? vb4.z : vb4.x, i ? vb4.w : vb4.y, pick);
+                    vs[n][0] = v.x;
+                    vs[n][1] = v.y;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t at = c ? t ^ 1 : t;
-                        const float ks = __uint_as_float(__byte_perm(kw[2 * i + c], 0u, 0x0444u | at << 12) >> 1);
-                        const float zero = ks - ks;
-#pragma unroll
-                        for (int hh = 0; hh < NH; ++hh) x[n][2 * hh + c] = fmaf(x[n][2 * hh + c], ks * rowf[hh], zero);
-                        // 2^23 + byte, as a float
-                        ve[n][c] = __uint_as_float(__byte_perm(vw[2 * i + c], 0x4b000000u, 0x7650u | at)) - 8388735.f;
+                    for (int hh = 0; hh < NH; ++hh) {
+                        x[n][2 * hh] *= ks.x;
+                        x[n][2 * hh + 1] *= ks.y;
                     }
                 }
             }
@@ -489,22 +508,14 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                     }
             }
             // ------------------------------------------------------------ softmax
-            float top[NH], high = ve[0][0];   // of x per row; of the V exponents
+            float top[NH];
             bool need = false;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) high = fmaxf(high, fmaxf(ve[n][0], ve[n][1]));
-            if (high > 100.f) {               // a V row that stands for NaN (or stale memory that is masked)
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        if (ve[n][c] > 100.f) ve[n][c] = __uint_as_float(0x7fc00000u);
-            }
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {
                 top[hh] = fmaxf(x[0][2 * hh], x[0][2 * hh + 1]);
 #pragma unroll
                 for (int n = 1; n < 4; ++n) top[hh] = fmaxf(top[hh], fmaxf(x[n][2 * hh], x[n][2 * hh + 1]));
+                top[hh] *= rowf[hh];
                 need |= top[hh] > m[hh] + kRescale;
             }
             if (__any_sync(0xffffffffu, need)) {
@@ -529,27 +540,29 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {
                 const float ref = m[hh] == -INFINITY ? 0.f : m[hh];
-                float y[4][2], yt = -INFINITY, sum = 0.f;
+                float p[4][2], top_w = 0.f, sum = 0.f;
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float xv = x[n][2 * hh + c];
-                        sum += ex2_approx(xv - ref);
-                        // a masked score stays -infinity, whatever the scale byte holds
-                        y[n][c] = all || xv != -INFINITY ? xv + ve[n][c] : -INFINITY;
-                        yt = fmaxf(yt, y[n][c]);
+                        const float e = ex2_approx(fmaf(xv, rowf[hh], -ref));
+                        sum += e;
+                        // a masked score stays -infinity and its w 0, whatever the scale byte holds
+                        p[n][c] = all || xv != -INFINITY ? e * vs[n][c] : 0.f;
+                        top_w = fmaxf(top_w, p[n][c]);
                     }
                 l[hh] += sum;
-                yt = fmaxf(yt, __shfl_xor_sync(0xffffffffu, yt, 1));
-                yt = fmaxf(yt, __shfl_xor_sync(0xffffffffu, yt, 2));
-                const float base = yt == -INFINITY ? 0.f : yt - 14.f;   // the largest w is 2^14
-                back[hh] = ex2_approx(base - ref);
+                top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 1));
+                top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 2));
+                // 2^k <= top_w < 2^(k + 1): scaled by 2^(14 - k), undone by back (k kept within -100 .. 100)
+                const int k = min(max((int)(__float_as_uint(top_w) >> 23), 27), 227);
+                const float up = pow2_of(268 - k);
+                back[hh] = pow2_of(k - 14);
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    pf[n][hh] = pack_half2(ex2_approx(y[n][0] - base), ex2_approx(y[n][1] - base));
+                for (int n = 0; n < 4; ++n) pf[n][hh] = pack_half2(p[n][0] * up, p[n][1] * up);
             }
-            // ------------------------------------------------------------ O += 2^(base - m) w V
+            // ------------------------------------------------------------ O += back (w up) V
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -683,6 +696,8 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
         }
         __syncthreads();
         if (tid < M * 2) (&poison[0][0])[tid] = 0u;
+        w.done();
+        more = w.next();
     }
     cp_wait<0>();
 }
@@ -768,7 +783,7 @@ template <bool FP8, int M>
 cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
     using C = Cfg<FP8, M>;
     auto kern = kv_rows_kernel<FP8, M>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(a.max_teams), kThreads, C::kSmem, st, a);
 }
@@ -777,24 +792,21 @@ cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
 
 template <int M>
 static cudaError_t launch_merge(const AttnArgs& a, cudaStream_t st) {
-    return launch_early(kv_merge_kernel<M>, dim3(a.max_teams * a.R, (a.mr + kMergeRows - 1) / kMergeRows), kMergeRows * 16,
-                        0, st, a);
+    return launch_early(kv_merge_kernel<M>, dim3(a.max_teams * a.R, (a.mr + kMergeRows - 1) / kMergeRows), kMergeRows * 16, 0,
+                        st, a);
 }
 
-cudaError_t launch_kv_merge128(const AttnArgs& a, cudaStream_t st) { return launch_merge<128>(a, st); }
+cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st) { return launch_merge<128>(a, st); }
 
 cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
-    cudaError_t e;
     a.R = 1;
     a.mr = eight ? 8 : 16;
     a.min_run = 1;
     a.set_divisors();
-    if (eight) {
-        e = fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st);
-        return e != cudaSuccess ? e : launch_merge<8>(a, st);
-    }
-    e = fp8 ? launch_rows<true, 16>(a, st) : launch_rows<false, 16>(a, st);
-    return e != cudaSuccess ? e : launch_merge<16>(a, st);
+    const cudaError_t e = eight ? (fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st))
+                                : (fp8 ? launch_rows<true, 16>(a, st) : launch_rows<false, 16>(a, st));
+    if (e != cudaSuccess) return e;
+    return eight ? launch_merge<8>(a, st) : launch_merge<16>(a, st);
 }
 
 }  // namespace bsa

@@ -593,14 +593,14 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, cons
     using C = Cfg<FP8>;
     const size_t smem = C::kOffCtl + (sizeof(Ctl) + 15) / 16 * 16;
     auto kern = kv_tc_kernel<FP8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(a.max_teams * a.R), C::kThreads, smem, st, q, k, v, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_merge128(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st);
 
 // Blocks per team. The R blocks of a team read the same keys at about the same time, so with
 // tiles query tiles per chunk the cache comes from HBM tiles / R times instead of tiles times;
@@ -636,7 +636,7 @@ cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
         return cudaErrorInvalidValue;
     }
     const cudaError_t e = fp8 ? launch<true>(a, q, k, v, st) : launch<false>(a, q, k, v, st);
-    return e != cudaSuccess ? e : launch_kv_merge128(a, st);
+    return e != cudaSuccess ? e : launch_kv_merge(a, st);
 }
 
 }  // namespace bsa

@@ -3,6 +3,8 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
+#include <vector>
 
 #include "common.cuh"
 
@@ -499,6 +501,25 @@ __device__ __forceinline__ float* part_at(const AttnArgs& a, int team, int run, 
 // and waits for that one's results first.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Allows a kernel its dynamic shared memory, once per kernel and device.
+inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    struct Done {
+        const void* kernel;
+        int device;
+    };
+    static std::mutex mutex;
+    static std::vector<Done> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const std::lock_guard<std::mutex> lock(mutex);
+    for (const Done& d : done)
+        if (d.kernel == kernel && d.device == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.push_back({kernel, dev});
+    return e;
+}
 
 template <class... P, class... A>
 inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
