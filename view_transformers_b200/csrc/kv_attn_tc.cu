@@ -34,6 +34,7 @@ using namespace kv;
 constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
+constexpr float kNone = -1e30f;                      // the reference before anything is seen: every p is 0
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kTile = 128 * 128;                // 128 rows of 64 bf16
 constexpr uint32_t kRawHalf = 128 * 64 + 128;        // 128 e4m3 rows of K or V and their scales
@@ -374,7 +375,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const Rec& rec = ctl.rec[X & 1];
             const int tiles = rec.tiles;
             if (tiles < 0) break;
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = kNone, l = 0.f;
             uint32_t poison0 = 0u, poison1 = 0u;   // columns that met a non-finite value of a key the row sees
             int lo = 0, hi = 0;
             if (row < rec.nrows) visible(a, rec.len, rec.pos0 + a.by_group.of(rec.r0 + row), lo, hi);
@@ -387,9 +388,8 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tmem_ld32(lane_base + kColS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
-                // done already (the product waited for it): orders the read of the tile's words
-                if (!warp_wait(&ctl.k_full[st], (U / NS) & 1, abort, a.status)) { ok = false; break; }
-                const int meta = ctl.meta[st];
+                // the tile's words: written before k_full, for which the product's thread waited
+                const int meta = *(volatile int*)&ctl.meta[st];
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
@@ -468,16 +468,15 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 const float mt2 = mt * kScaleLog2;
                 const bool need = mt2 > m_ref + kRescale;
-                const bool corr = need && m_ref != -INFINITY;
+                const bool corr = need && m_ref != kNone;
                 const float new_ref = need ? mt2 : m_ref;
                 const float factor = corr ? ex2_approx(m_ref - new_ref) : 1.f;
                 m_ref = new_ref;
-                const float ref = m_ref == -INFINITY ? 0.f : m_ref;   // nothing seen yet: every p is 0
                 float2 r2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r2[i] = make_float2(0.f, 0.f);
                 const float2 scale2 = make_float2(kScaleLog2, kScaleLog2);
-                const float2 shift2 = make_float2(-ref, -ref);
+                const float2 shift2 = make_float2(-m_ref, -m_ref);
 #pragma unroll
                 for (int c = 0; c < 128; c += 2) {
                     const int i = c / 2;
