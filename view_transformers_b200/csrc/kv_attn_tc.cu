@@ -248,58 +248,69 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
         } else if (warp == 1) {
             // ======================================================== MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_qk = idesc_f16(128, 128, 1u, false);
-                constexpr uint32_t idesc_pv = idesc_f16(128, 64, 1u, true);
-                const uint32_t q_base = smem_u32(smem + C::kOffQ);
-                auto issue_qk = [&](int U) {
-                    const uint32_t k_base = smem_u32(smem + C::kOffK + (U % NS) * kTile);
+            // The whole warp runs the loop, so that addresses and descriptors are uniform values, and one
+            // lane issues. (With one lane in the loop, issuing a tile's ten products and commits took
+            // 1,100 clocks, and this thread, not the exponentials, set the pace.)
+            const bool leader = elect_one();
+            constexpr uint32_t idesc_qk = idesc_f16(128, 128, 1u, false);
+            constexpr uint32_t idesc_pv = idesc_f16(128, 64, 1u, true);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::kOffV), 0, 1024);
+            auto issue_qk = [&](int st) {
+                if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ss(tmem + kColS, sdesc_sw128(q_base + 32 * ks, 16, 1024),
-                               sdesc_sw128(k_base + 32 * ks, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
+                    for (int ks = 0; ks < 4; ++ks)   // 32 bytes a step, in 16-byte units
+                        mma_ss(tmem + kColS, q_desc + 2 * ks, k_desc + (uint64_t)(st * (kTile >> 4)) + 2 * ks, idesc_qk,
+                               ks > 0 ? 1u : 0u);
                     mma_commit(&ctl.s_full);
-                };
-                int I = 0, meta = 0;
-                bool fresh = true;             // tile U starts a segment
-                for (int U = 0;; ++U) {
-                    const int st = U % NS;
-                    if (fresh) {                   // within a segment its QK^T is issued already
-                        if (!mbar_wait(&ctl.k_full[st], (U / NS) & 1, abort, a.status)) break;
-                        meta = ctl.meta[st];
-                        if (meta & kEnd) break;
-                        if (!mbar_wait(&ctl.q_full, I & 1, abort, a.status)) break;
-                        ++I;
-                        // the previous segment's last S has been read by the softmax
-                        if (U > 0 && !mbar_wait(&ctl.s_free, (U - 1) & 1, abort, a.status)) break;
-                        tc_fence_after();
-                        issue_qk(U);
-                    }
-                    const int cur = meta;
-                    fresh = (cur & kLast) != 0;
-                    if (!fresh) {
-                        const int sn = (U + 1) % NS;
-                        if (!mbar_wait(&ctl.s_free, U & 1, abort, a.status) ||
-                            !mbar_wait(&ctl.k_full[sn], ((U + 1) / NS) & 1, abort, a.status))
-                            break;
-                        tc_fence_after();
-                        issue_qk(U + 1);
-                        meta = ctl.meta[sn];
-                    } else {
-                        mma_commit(&ctl.q_empty);   // the segment's last Q K^T is issued
-                    }
-                    if (FP8 && !mbar_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) break;
-                    if (!mbar_wait(&ctl.p_full, U & 1, abort, a.status)) break;
+                }
+                __syncwarp();
+            };
+            int I = 0, meta = 0, st = 0;
+            uint32_t turn = 0u;            // parity of the stage's use
+            bool fresh = true;             // tile U starts a segment
+            for (int U = 0;; ++U) {
+                if (fresh) {               // within a segment its QK^T is issued already
+                    if (!warp_wait(&ctl.k_full[st], turn, abort, a.status)) break;
+                    meta = *(volatile int*)&ctl.meta[st];
+                    if (meta & kEnd) break;
+                    if (!warp_wait(&ctl.q_full, I & 1, abort, a.status)) break;
+                    ++I;
+                    // the previous segment's last S has been read by the softmax
+                    if (U > 0 && !warp_wait(&ctl.s_free, (U - 1) & 1, abort, a.status)) break;
                     tc_fence_after();
-                    const uint32_t v_base = smem_u32(smem + C::kOffV + st * kTile);
+                    issue_qk(st);
+                }
+                const int cur = meta;
+                const int sn = st + 1 == NS ? 0 : st + 1;
+                const uint32_t tn = st + 1 == NS ? turn ^ 1u : turn;
+                fresh = (cur & kLast) != 0;
+                if (!fresh) {
+                    if (!warp_wait(&ctl.k_full[sn], tn, abort, a.status) ||
+                        !warp_wait(&ctl.s_free, U & 1, abort, a.status))
+                        break;
+                    tc_fence_after();
+                    issue_qk(sn);
+                    meta = *(volatile int*)&ctl.meta[sn];
+                } else if (leader) {
+                    mma_commit(&ctl.q_empty);   // the segment's last Q K^T is issued
+                }
+                if (FP8 && !warp_wait(&ctl.v_full[st], turn, abort, a.status)) break;
+                if (!warp_wait(&ctl.p_full, U & 1, abort, a.status)) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem + kColO, tmem + kColP + 8 * ks, sdesc_sw128(v_base + 2048 * ks, 0, 1024), idesc_pv,
+                    for (int ks = 0; ks < 8; ++ks)   // 16 rows of 128 bytes a step
+                        mma_ts(tmem + kColO, tmem + kColP + 8 * ks, v_desc + (uint64_t)(st * (kTile >> 4)) + 128 * ks, idesc_pv,
                                (!(cur & kFirst) || ks > 0) ? 1u : 0u);
                     mma_commit(&ctl.kv_empty[st]);
                     mma_commit(&ctl.o_done);
                     if (fresh) mma_commit(&ctl.o_final);
                 }
+                __syncwarp();
+                st = sn;
+                turn = tn;
             }
         } else if (FP8) {
             // ======================================================== e4m3 -> bf16
@@ -572,7 +583,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int u = max(0, issued - ring); u < issued; ++u)
                 mbar_wait(FP8 ? &ctl.raw_full[u % ring] : &ctl.k_full[u % ring], (u / ring) & 1, &never, a.status, kDrainNs);
         }
-        if (warp == 1 && lane == 0) {
+        if (warp == 1 && elect_one()) {   // the thread that issued the products
             mma_commit(&ctl.drain);
             mbar_wait(&ctl.drain, 0, &never, a.status, kDrainNs);
         }
