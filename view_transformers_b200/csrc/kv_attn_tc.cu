@@ -44,8 +44,7 @@ constexpr uint64_t kDrainNs = 50000000ull;
 template <bool FP8>
 struct Cfg {
     static constexpr int NS = FP8 ? 2 : 3;           // K/V stages
-    static constexpr int kThreads = FP8 ? 256 : 192;
-    static constexpr int kSoftmaxWarp = FP8 ? 4 : 2; // first of the four softmax warps
+    static constexpr int kThreads = 256;             // warps 4 .. 7: softmax
     static constexpr uint32_t kOffQ = 0;
     static constexpr uint32_t kOffK = kTile;
     static constexpr uint32_t kOffV = kOffK + NS * kTile;
@@ -160,9 +159,15 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     int issued = 0;         // K/V tiles (e4m3: half tiles) whose loads the producer issued
     int q_loads = 0;        // Q tiles the producer issued
 
-    if (warp < C::kSoftmaxWarp) {
-        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 0) {
+    // Roles 0 (producer), 1 (products), 2 and 3 (e4m3: conversion) of warps 0 .. 3. A warp's scheduler is
+    // its number modulo 4, for the softmax's four too, so the two blocks of an SM (told apart by
+    // where their tensor memory lies) take the roles in opposite halves: each scheduler then has
+    // one busy role besides two softmax warps, and no row quarter of a tile trails the others.
+    const int role = warp < 4 ? (tmem & 0xffffu ? warp ^ 2 : warp) : 4;
+
+    if (role < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (role == 0) {
             // ======================================================== producer
             int U = 0, I = 0, X = 0;     // tiles, Q tiles, segments so far
             auto put_record = [&](const Rec& r) -> bool {
@@ -246,7 +251,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     put_record(rec);
                 }
             }
-        } else if (warp == 1) {
+        } else if (role == 1) {
             // ======================================================== MMA issuer
             // The whole warp runs the loop, so that addresses and descriptors are uniform values, and one
             // lane issues. (With one lane in the loop, issuing a tile's ten products and commits took
@@ -316,7 +321,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // ======================================================== e4m3 -> bf16
             // four lanes share a row of 64 codes; each writes two 16-byte chunks of the swizzled
             // bf16 row. Rows of pages that do not exist are left as they are.
-            const int cw = warp - 2;
+            const int cw = role - 2;
             bool ok = true;
             for (int U = 0; ok; ++U) {
                 const int st = U % NS;
@@ -368,7 +373,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
     } else {
         // ============================================================ softmax + epilogue
-        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -577,13 +582,13 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     __syncthreads();
     if (ctl.abort) {
         volatile int never = 0;
-        if (warp == 0 && lane == 0) {
+        if (role == 0 && lane == 0) {
             if (q_loads > 0) mbar_wait(&ctl.q_full, (q_loads - 1) & 1, &never, a.status, kDrainNs);
             constexpr int ring = FP8 ? kRaw : NS;
             for (int u = max(0, issued - ring); u < issued; ++u)
                 mbar_wait(FP8 ? &ctl.raw_full[u % ring] : &ctl.k_full[u % ring], (u / ring) & 1, &never, a.status, kDrainNs);
         }
-        if (warp == 1 && elect_one()) {   // the thread that issued the products
+        if (role == 1 && elect_one()) {   // the thread that issued the products
             mma_commit(&ctl.drain);
             mbar_wait(&ctl.drain, 0, &never, a.status, kDrainNs);
         }
