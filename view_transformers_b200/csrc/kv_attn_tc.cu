@@ -44,7 +44,9 @@ constexpr uint64_t kDrainNs = 50000000ull;
 template <bool FP8>
 struct Cfg {
     static constexpr int NS = FP8 ? 2 : 3;           // K/V stages
-    static constexpr int kThreads = 256;             // warps 4 .. 7: softmax
+    // warps 0 .. 3: producer, products; 4 .. 7: softmax; 8 .. 11: e4m3 conversion. Registers a thread
+    // of each four, together what the block is launched with (128 and 80 a thread)
+    static constexpr int kThreads = FP8 ? 384 : 256;
     static constexpr uint32_t kOffQ = 0;
     static constexpr uint32_t kOffK = kTile;
     static constexpr uint32_t kOffV = kOffK + NS * kTile;
@@ -61,7 +63,7 @@ struct Ctl {
     Rec rec[2];
     int meta[3], tile[3];                            // of the stages
     int raw_meta[kRaw], raw_tile[kRaw];
-    int found;                                       // the last tile (count) with values taken out
+    int found[2];                                    // the last even, odd tile with values taken out, plus 1
     uint32_t tmem_base;
     int abort;
     Start start;
@@ -118,13 +120,13 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&ctl.q_full, 1);
         mbar_init(&ctl.q_empty, 1);
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&ctl.k_full[s], FP8 ? 2 : 1);
-            mbar_init(&ctl.v_full[s], 2);
+            mbar_init(&ctl.k_full[s], FP8 ? 4 : 1);
+            mbar_init(&ctl.v_full[s], 4);
             mbar_init(&ctl.kv_empty[s], 1);
         }
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&ctl.raw_full[s], 1);
-            mbar_init(&ctl.raw_empty[s], 2);
+            mbar_init(&ctl.raw_empty[s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl.rec_full[s], 1);
@@ -137,7 +139,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&ctl.o_final, 1);
         mbar_init(&ctl.drain, 1);
         mbar_init(&ctl.meet, 4);
-        ctl.found = 0;
+        ctl.found[0] = ctl.found[1] = 0;
         ctl.abort = 0;
         fence_mbar_init();
     }
@@ -159,14 +161,15 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     int issued = 0;         // K/V tiles (e4m3: half tiles) whose loads the producer issued
     int q_loads = 0;        // Q tiles the producer issued
 
-    // Roles 0 (producer), 1 (products), 2 and 3 (e4m3: conversion) of warps 0 .. 3. A warp's scheduler is
-    // its number modulo 4, for the softmax's four too, so the two blocks of an SM (told apart by
-    // where their tensor memory lies) take the roles in opposite halves: each scheduler then has
-    // one busy role besides two softmax warps, and no row quarter of a tile trails the others.
-    const int role = warp < 4 ? (tmem & 0xffffu ? warp ^ 2 : warp) : 4;
+    // Roles 0 (producer) and 1 (products) of warps 0 .. 3, 4: softmax, 5: conversion. A warp's scheduler
+    // is its number modulo 4, for the softmax's four too, so the two blocks of an SM (told apart by
+    // where their tensor memory lies) take the roles in opposite halves: no row quarter of a tile
+    // then trails the others.
+    const int role = warp >= 8 ? 5 : warp >= 4 ? 4 : tmem & 0xffffu ? warp ^ 2 : warp;
 
     if (role < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (role == 0) {
             // ======================================================== producer
             int U = 0, I = 0, X = 0;     // tiles, Q tiles, segments so far
@@ -317,63 +320,65 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 st = sn;
                 turn = tn;
             }
-        } else if (FP8) {
-            // ======================================================== e4m3 -> bf16
-            // four lanes share a row of 64 codes; each writes two 16-byte chunks of the swizzled
-            // bf16 row. Rows of pages that do not exist are left as they are.
-            const int cw = role - 2;
-            bool ok = true;
-            for (int U = 0; ok; ++U) {
-                const int st = U % NS;
-                if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) break;
+        }
+    } else if (FP8 && role == 5) {
+        // ============================================================ e4m3 -> bf16
+        // four lanes share a row of 64 codes; each writes two 16-byte chunks of the swizzled
+        // bf16 row. Rows of pages that do not exist are left as they are.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int cw = warp - 8;
+        bool ok = true;
+        for (int U = 0; ok; ++U) {
+            const int st = U % NS;
+            if (U >= NS && !warp_wait(&ctl.kv_empty[st], ((U / NS) - 1) & 1, abort, a.status)) break;
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int x = 2 * U + half, slot = x % kRaw;
-                    if (!warp_wait(&ctl.raw_full[slot], (x / kRaw) & 1, abort, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t* src = smem + C::kOffRaw + slot * kRawHalf;
-                    uint8_t* dst = smem + (half ? C::kOffV : C::kOffK) + st * kTile;
-                    const int meta = ctl.raw_meta[slot];
-                    if (cw == 0 && lane == 0 && half == 0) {
-                        ctl.meta[st] = meta;
-                        ctl.tile[st] = ctl.raw_tile[slot];
-                    }
-                    if (meta & kEnd) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl.k_full[st]);
-                        ok = false;
-                        break;
-                    }
-#pragma unroll 4
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 16 + cw * 8 + (lane >> 2);
-                        if ((meta >> i) & 1) {
-                            const uint4 c = *reinterpret_cast<const uint4*>(src + r * 64 + (lane & 3) * 16);
-                            const uint32_t b = src[8192 + r];
-                            const float f = scale_of(b);
-                            const int c0 = 2 * (lane & 3);
-                            *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) * 16)) =
-                                make_uint4(bf16_of(c.x, false, f), bf16_of(c.x, true, f), bf16_of(c.y, false, f),
-                                           bf16_of(c.y, true, f));
-                            *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) * 16)) =
-                                make_uint4(bf16_of(c.z, false, f), bf16_of(c.z, true, f), bf16_of(c.w, false, f),
-                                           bf16_of(c.w, true, f));
-                        }
-                    }
-                    fence_async_shared();
+            for (int half = 0; half < 2; ++half) {
+                const int x = 2 * U + half, slot = x % kRaw;
+                if (!warp_wait(&ctl.raw_full[slot], (x / kRaw) & 1, abort, a.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* src = smem + C::kOffRaw + slot * kRawHalf;
+                uint8_t* dst = smem + (half ? C::kOffV : C::kOffK) + st * kTile;
+                const int meta = ctl.raw_meta[slot];
+                if (cw == 0 && lane == 0 && half == 0) {
+                    ctl.meta[st] = meta;
+                    ctl.tile[st] = ctl.raw_tile[slot];
+                }
+                if (meta & kEnd) {
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(half ? &ctl.v_full[st] : &ctl.k_full[st]);
-                        mbar_arrive(&ctl.raw_empty[slot]);
+                    if (lane == 0) mbar_arrive(&ctl.k_full[st]);
+                    ok = false;
+                    break;
+                }
+#pragma unroll 4
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 32 + cw * 8 + (lane >> 2);
+                    if ((meta >> (r >> 4)) & 1) {
+                        const uint4 c = *reinterpret_cast<const uint4*>(src + r * 64 + (lane & 3) * 16);
+                        const uint32_t b = src[8192 + r];
+                        const float f = scale_of(b);
+                        const int c0 = 2 * (lane & 3);
+                        *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) * 16)) =
+                            make_uint4(bf16_of(c.x, false, f), bf16_of(c.x, true, f), bf16_of(c.y, false, f),
+                                       bf16_of(c.y, true, f));
+                        *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) * 16)) =
+                            make_uint4(bf16_of(c.z, false, f), bf16_of(c.z, true, f), bf16_of(c.w, false, f),
+                                       bf16_of(c.w, true, f));
                     }
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(half ? &ctl.v_full[st] : &ctl.k_full[st]);
+                    mbar_arrive(&ctl.raw_empty[slot]);
                 }
             }
         }
     } else {
         // ============================================================ softmax + epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -397,26 +402,47 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int st = U % NS;
                 if (!warp_wait(&ctl.s_full, U & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t s[128];
+                // bf16: S in 128 registers. e4m3: half of it at a time, the first half read again for its
+                // exponentials, so that 128 registers a thread do and four warps can convert.
+                uint32_t s[FP8 ? 1 : 2][64];
+                auto load = [&](uint32_t(&x)[64], int c0) {
+                    tmem_ld32(lane_base + kColS + c0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                    tmem_ld32(lane_base + kColS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                };
+                auto s_is_read = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.s_free);
+                };
+                auto top_of = [&](const uint32_t(&x)[64]) {
+                    float acc[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(lane_base + kColS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+                    for (int i = 0; i < 4; ++i) acc[i] = __uint_as_float(x[i]);
+#pragma unroll
+                    for (int c = 4; c < 64; c += 2)
+                        acc[(c / 2) & 3] = max3f(acc[(c / 2) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                    return fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3]));
+                };
+                auto hide = [&](uint32_t(&x)[64], uint32_t see0, uint32_t see1) {   // what the row does not see
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (!(((c < 32 ? see0 : see1) >> (c & 31)) & 1u)) x[c] = 0xff800000u;   // -infinity
+                };
+                load(s[0], 0);
+                if (!FP8) load(s[FP8 ? 0 : 1], 64);
                 // the tile's words: written before k_full, for which the product's thread waited
                 const int meta = *(volatile int*)&ctl.meta[st];
                 tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.s_free);
-                float mt = -INFINITY;
+                if (!FP8) s_is_read();
+                float mt;
                 uint32_t see[4];
                 if (meta & kFull) {
-                    float acc[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] = __uint_as_float(s[i]);
-#pragma unroll
-                    for (int c = 8; c < 128; c += 2)
-                        acc[(c / 2) & 7] = max3f(acc[(c / 2) & 7], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                    mt = max3f(max3f(acc[0], acc[1], acc[2]), max3f(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
+                    mt = top_of(s[0]);
+                    if (FP8) {
+                        load(s[0], 64);
+                        tmem_wait_ld();
+                    }
+                    mt = fmaxf(mt, top_of(s[FP8 ? 0 : 1]));
                 } else {
                     // columns of this row that count
                     const int k0 = ctl.tile[st] * kUnit;
@@ -425,12 +451,15 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         const int b = k0 + 32 * k;
                         see[k] = low_bits(hi - b) & (~low_bits(lo - b) | low_bits(a.sink - b)) &
                                  (((meta >> (2 * k)) & 1 ? 0xffffu : 0u) | ((meta >> (2 * k + 1)) & 1 ? 0xffff0000u : 0u));
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (!((see[k] >> c) & 1u)) s[32 * k + c] = 0xff800000u;   // -infinity
-                            mt = fmaxf(mt, __uint_as_float(s[32 * k + c]));
-                        }
                     }
+                    hide(s[0], see[0], see[1]);
+                    mt = top_of(s[0]);
+                    if (FP8) {
+                        load(s[0], 64);
+                        tmem_wait_ld();
+                    }
+                    hide(s[FP8 ? 0 : 1], see[2], see[3]);
+                    mt = fmaxf(mt, top_of(s[FP8 ? 0 : 1]));
                     // V of key k0 + row: P = 0 does not silence what is not finite
                     if (FP8 && !warp_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) { ok = false; break; }
                     uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * kTile + row * 128);
@@ -460,10 +489,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                         for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    // rare: K's tile is done with (S is read), so its memory passes the columns on
-                    if (bad0 | bad1) ctl.found = U + 1;
+                    // rare: K's tile is done with (S is there), so its memory passes the columns on
+                    if (bad0 | bad1) ctl.found[U & 1] = U + 1;
                     if (!meet()) { ok = false; break; }
-                    if (*(volatile int*)&ctl.found == U + 1) {
+                    if (*(volatile int*)&ctl.found[U & 1] == U + 1) {
                         uint2* list = reinterpret_cast<uint2*>(smem + C::kOffK + st * kTile);
                         list[row] = make_uint2(bad0, bad1);
                         if (!meet()) { ok = false; break; }
@@ -490,18 +519,19 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int i = 0; i < 4; ++i) r2[i] = make_float2(0.f, 0.f);
                 const float2 scale2 = make_float2(kScaleLog2, kScaleLog2);
                 const float2 shift2 = make_float2(-m_ref, -m_ref);
+                auto weigh = [&](uint32_t(&x)[64]) {   // 64 scores to 32 pairs of weights, in place
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) {
-                    const int i = c / 2;
-                    const float2 x =
-                        __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, shift2);
-                    const float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                    r2[i & 3] = __fadd2_rn(r2[i & 3], pr);
-                    s[i] = pack_bf16(pr.x, pr.y);
-                }
-                const float rs =
-                    ((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y));
-                l = l * factor + rs;
+                    for (int c = 0; c < 64; c += 2) {
+                        const int i = c / 2;
+                        const float2 y =
+                            __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2);
+                        const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        r2[i & 3] = __fadd2_rn(r2[i & 3], pr);
+                        x[i] = pack_bf16(pr.x, pr.y);
+                    }
+                };
+                if (!FP8) weigh(s[0]);
+                weigh(s[FP8 ? 0 : 1]);
                 // P.V of the item's previous tile must be done before O is rescaled or P is
                 // overwritten (for the first tile, the previous item's o_final wait covered it)
                 if (u > 0 && !warp_wait(&ctl.o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
@@ -517,9 +547,16 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         tmem_st32(lane_base + kColO + 32 * k, o);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    tmem_st32(lane_base + kColP + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(&s[32 * c]));
+                tmem_st32(lane_base + kColP + 32, *reinterpret_cast<const uint32_t(*)[32]>(&s[FP8 ? 0 : 1][0]));
+                if (FP8) {
+                    load(s[0], 0);
+                    tmem_wait_ld();
+                    s_is_read();
+                    if (!(meta & kFull)) hide(s[0], see[0], see[1]);
+                    weigh(s[0]);
+                }
+                tmem_st32(lane_base + kColP, *reinterpret_cast<const uint32_t(*)[32]>(&s[0][0]));
+                l = l * factor + (((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y)));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
