@@ -97,14 +97,18 @@ class KVCache:
                                    page_table.shape[1], _lib.KV_FORMATS[self.fmt], ptr(k), ptr(v), ptr(k_scale),
                                    ptr(v_scale), ptr(page_table), ptr(kv_len))
         self.seqs = page_table.shape[0]
-        with self._on_device():
+        self._index = self.device.index
+        with torch.cuda.device(self.device) if self.device.type == "cuda" else contextlib.nullcontext():
             self.ws_bytes = _lib.bsa_kv_workspace_size(self.c)
+        self._lib = _lib.load()
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ref = ctypes.byref(self.c)
         self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
 
     # steps --------------------------------------------------------------------------
+    # A short call is over on the GPU in a few microseconds, so what happens here per call is kept
+    # to the checks themselves.
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, stream: int | None = None) -> None:
         """Writes the new tokens' keys and values ([rows, kv_heads, 64] bf16, one row stride) to the ends
         of their sequences, whose kv_len and pages count them already."""
@@ -112,10 +116,8 @@ class KVCache:
         if self._rows("v", v, self.kv_heads) != (rows, stride):
             raise ValueError("k and v must have the same rows and row stride")
         self._offsets("cu_new", cu_new, self.seqs + 1)
-        st, guard = self._stream(stream)
-        with guard:
-            _lib._check("bsa_kv_append", _lib.load().bsa_kv_append(
-                self._ref, rows, cu_new.data_ptr(), k.data_ptr(), v.data_ptr(), stride, self._status_ptr, st))
+        self._call("bsa_kv_append", self._lib.bsa_kv_append, stream, rows, cu_new.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   stride, self._status_ptr)
 
     def attend(self, q: torch.Tensor, cu_new: torch.Tensor, max_new: int, unit: int = 0, window: int = 0,
                sink: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -132,16 +134,16 @@ class KVCache:
         out_rows, out_stride = self._rows("out", out, self.heads)
         if out_rows != rows:
             raise ValueError("out must have q's rows")
-        if lse is not None and (lse.shape != (self.heads, rows) or lse.dtype != torch.float32
-                                or lse.device != self.device or not lse.is_contiguous()):
-            raise ValueError(f"lse must be a contiguous float32 tensor {(self.heads, rows)} on {self.device}")
+        lse_ptr = None
+        if lse is not None:
+            if (lse.shape != (self.heads, rows) or lse.dtype is not torch.float32 or lse.device != self.device
+                    or not lse.is_contiguous()):
+                raise ValueError(f"lse must be a contiguous float32 tensor {(self.heads, rows)} on {self.device}")
+            lse_ptr = lse.data_ptr()
         self._offsets("cu_new", cu_new, self.seqs + 1)
-        st, guard = self._stream(stream)
-        with guard:
-            _lib._check("bsa_kv_attention", _lib.load().bsa_kv_attention(
-                self._ref, rows, max_new, unit, window, sink, cu_new.data_ptr(), q.data_ptr(), stride,
-                out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), self._ws_ptr, self.ws_bytes,
-                self._status_ptr, st))
+        self._call("bsa_kv_attention", self._lib.bsa_kv_attention, stream, rows, max_new, unit, window, sink,
+                   cu_new.data_ptr(), q.data_ptr(), stride, out.data_ptr(), out_stride, lse_ptr, self._ws_ptr,
+                   self.ws_bytes, self._status_ptr)
         return out
 
     def read(self, cu_rows: torch.Tensor, first: torch.Tensor, rows: int | None = None, out=None,
@@ -162,18 +164,14 @@ class KVCache:
             raise ValueError("k and v must have the same rows and row stride")
         self._offsets("cu_rows", cu_rows, self.seqs + 1)
         self._offsets("first", first, self.seqs)
-        st, guard = self._stream(stream)
-        with guard:
-            _lib._check("bsa_kv_read", _lib.load().bsa_kv_read(
-                self._ref, n, cu_rows.data_ptr(), first.data_ptr(), k.data_ptr(), v.data_ptr(), stride,
-                self._status_ptr, st))
+        self._call("bsa_kv_read", self._lib.bsa_kv_read, stream, n, cu_rows.data_ptr(), first.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), stride, self._status_ptr)
         return k, v
 
     def check_status(self, stream: int | None = None) -> int:
         """Waits for the stream; the first device-side error since the last check (0: none)."""
-        st, guard = self._stream(stream)
-        with guard:
-            return _lib.bsa_check_status(self._status_ptr, st)
+        with torch.cuda.device(self.device):
+            return _lib.bsa_check_status(self._status_ptr, _raw_stream(self._index) if stream is None else stream)
 
     # pages and lengths kept by the cache itself ------------------------------------------
     def extend(self, counts, stream: int | None = None) -> Chunk:
@@ -240,24 +238,27 @@ class KVCache:
 
     def _rows(self, name: str, x: torch.Tensor, heads: int) -> tuple[int, int]:
         shape, stride = x.shape, x.stride()
-        if (len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim or x.dtype != torch.bfloat16
+        if (len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim or x.dtype is not torch.bfloat16
                 or x.device != self.device or stride[2] != 1 or stride[1] != self.head_dim):
             raise ValueError(f"{name} must be a bf16 tensor [rows, {heads}, {self.head_dim}] on {self.device} whose "
                              "rows are contiguous")
         return shape[0], stride[0] if shape[0] > 1 else heads * self.head_dim
 
     def _offsets(self, name: str, x: torch.Tensor, n: int) -> None:
-        if x.dtype != torch.int32 or x.shape != (n,) or x.device != self.device or not x.is_contiguous():
+        if x.dtype is not torch.int32 or x.dim() != 1 or len(x) != n or x.device != self.device or not x.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
 
-    def _on_device(self):
-        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
-
-    def _stream(self, stream):
-        st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
-        return st, self._on_device()
+    def _call(self, name: str, fn, stream, *args) -> None:
+        """fn(cache, *args, stream) on the cache's device, on its current stream unless one is given."""
+        if stream is None:
+            stream = _raw_stream(self._index)
+        if _current_device() == self._index:
+            code = fn(self._ref, *args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                code = fn(self._ref, *args, stream)
+        if code:
+            _lib._check(name, code)
 
     def _torch_stream(self, stream):
         if stream is None:
@@ -268,3 +269,10 @@ class KVCache:
 def _device(device) -> torch.device:
     dev = torch.device(device)
     return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
+
+
+# current_stream().cuda_stream and current_device() without the objects in between (several
+# microseconds a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
