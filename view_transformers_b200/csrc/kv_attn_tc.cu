@@ -168,7 +168,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     const int role = warp >= 8 ? 5 : warp >= 4 ? 4 : tmem & 0xffffu ? warp ^ 2 : warp;
 
     if (role < 4) {
-        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (role == 0) {
             // ======================================================== producer
@@ -377,7 +377,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
     } else {
         // ============================================================ softmax + epilogue
-        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
@@ -403,7 +403,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (!warp_wait(&ctl.s_full, U & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
                 // bf16: S in 128 registers. e4m3: half of it at a time, the first half read again for its
-                // exponentials, so that 128 registers a thread do and four warps can convert.
+                // exponentials, so that 136 registers a thread do and four warps can convert.
                 uint32_t s[FP8 ? 1 : 2][64];
                 auto load = [&](uint32_t(&x)[64], int c0) {
                     tmem_ld32(lane_base + kColS + c0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
