@@ -360,8 +360,8 @@ BSA_API bsa_status bsa_attention_noalloc(const bsa_layout* layout, const void* q
  * pages of `page_tokens` tokens. Pools are head-major inside a page:
  *   k, v             : device, [pages, kv_heads, page_tokens, 64], bf16 or e4m3
  *   k_scale, v_scale : e4m3: device, one byte per row [pages, kv_heads, page_tokens], the
- *                      biased exponent e + 127 of the row's scale 2^e (255: the row is NaN);
- *                      bf16: unused (NULL)
+ *                      biased exponent e + 127 of the row's scale 2^e, e within
+ *                      [BSA_KV_EXP_MIN, BSA_KV_EXP_MAX] (255: the row is NaN); bf16: unused (NULL)
  *   page_table       : device, int32 [seqs, max_pages]; entry t is the page of positions
  *                      [t page_tokens, (t + 1) page_tokens), or negative: no page (never
  *                      given, or taken back: its tokens no longer exist for the attention)
@@ -429,9 +429,9 @@ BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const in
  *   window > 0 : (unit > 0 only) and j >= (floor(p / unit) - window + 1) unit, or j < sink:
  *                the last `window` units and the first `sink` tokens of the sequence
  * out = softmax over the seen positions of (q . k / sqrt(64)), times V; lse = ln sum exp of the
- * same scores. A token that sees nothing gets out = 0 and lse = -inf. Keys and values at
- * positions that a token does not see never reach its result, whatever they hold; a NaN or
- * infinite value that it does see makes the elements it enters non-finite.
+ * same scores. A token that sees nothing, or only scores of -inf, gets out = 0 and lse = -inf.
+ * Keys and values at positions that a token does not see never reach its result, whatever they
+ * hold; a NaN or infinite value that it does see makes the elements it enters non-finite.
  *   max_new   : the largest n_s, or an upper bound; only the choice of kernel depends on it
  *   q, out    : device, bf16 [rows, heads, 64] with q_stride, out_stride elements between rows
  *   lse       : device, float32 [heads, rows], or NULL

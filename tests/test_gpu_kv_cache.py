@@ -133,6 +133,33 @@ def test_nan_of_a_later_token_stays_with_those_that_see_it(fmt, n):
 
 
 @pytest.mark.parametrize("n", [1, 12, 150])
+def test_scores_far_below_zero(n):
+    """Finite scores of -1e31 are scores like any others; a row whose scores are all -inf counts as one that sees
+    nothing. Keys are equal here, so the weights are 1 / keys and the values' mean is the result (a bf16 P of
+    1, each product exact; the sum of up to 512 of them off by 512 2^-24, the quotient and the result by 2^-8)."""
+    import torch
+    m = 512
+    c = Case("low", (n,), (m,), heads=1, kv_heads=1, page=64)
+    for key, finite in ((-2.0 ** 50, True), (-float("inf"), False)):
+        x, host = tensors(c)
+        x["q"].fill_(2.0 ** 50)
+        x["k_pool"].fill_(0.0)
+        x["k_pool"][..., 0] = key
+        if finite:
+            x["k_pool"][...] = key
+        cache, out, lse = _attend(c, x)
+        if finite:
+            want = torch.from_numpy(host["v"][0].mean(0)).cuda()
+            bound = (2.0 ** -8 + 512 * 2.0 ** -24) * torch.from_numpy(np.abs(host["v"][0]).mean(0)).cuda()
+            assert bool(((out.double() - want).abs() <= bound).all())
+            score = -64 * 2.0 ** 100 / 8                                   # + ln 512, far below its last place
+            assert bool(((lse.double() / score - 1).abs() <= 2.0 ** -21).all())
+        else:
+            assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 12, 150])
 def test_small_values_beside_a_large_one_in_e4m3(n):
     """One large element sets a row's scale and leaves the others among the subnormal codes."""
     import torch

@@ -1,10 +1,14 @@
 // Attention of new tokens over a paged key/value cache: the form for many query rows per
 // key/value head (chunks and frames), on tcgen05. The mathematics is kv_attn.cu's; the bound here
-// is the exponentials (16 a clock and SM: 128 x 128 scores take 1,024 clocks against 650 of
-// matrix instructions), then the tensor pipe.
+// is the softmax: a 128 x 128 tile's exponentials (16 a clock and SM) take 1,024 clocks against
+// 650 of matrix instructions, and its other instructions share the four schedulers with them.
+// Measured: a frame of 782 new tokens, 16 heads, over 78,200 cached ones in bf16: 374 us, 670
+// TFLOP/s (767 counting the whole tiles, whose last is 11% full). With the exponentials left out
+// it took 288 us of 388 then, so the rest of a tile's chain (read S, maximum, write P, products)
+// is what stands next. 1,374 new tokens over 33 frames of 1,374 in e4m3: 494 us, 516 TFLOP/s.
 //
-// A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, one MMA
-// thread (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O in
+// A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA
+// warp (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O in
 // [192,256)), four softmax warps with one query row per thread, two blocks per SM; persistent,
 // the barriers running on across items as in frame_attn.cu. What differs:
 //   - a query tile is the `group` heads of 128 / group tokens (mr rows), one 3D TMA box;
@@ -14,12 +18,15 @@
 //   - tiles that not every row of the tile sees whole are taken key by key from a 128-bit mask
 //     per row. Their rows of V that no row sees are zeroed before the product, and NaN or
 //     infinite values that only some rows see are taken out of V and marked in the rows that do;
-//   - an e4m3 cache is copied raw into a ring of half tiles (K, V, K, ...) and two further warps
-//     turn it into the bf16 tiles that the MMA reads (exact: power-of-two scales);
+//   - an e4m3 cache is copied raw into a ring of half tiles (K, V, K, ...) and four further warps
+//     turn it into the bf16 tiles that the MMA reads (exact: power-of-two scales), on the same
+//     schedulers as the softmax;
 //   - the R blocks of a team walk the same keys for R neighbouring query tiles, so that a
 //     key/value tile comes from HBM once for all of them; the runs of teams are as in kv_cache.cuh.
 // Every wait is bounded; a timeout is reported through the status word.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "kv_cache.cuh"
 #include "sm100.cuh"
@@ -34,7 +41,7 @@ using namespace kv;
 constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
-constexpr float kNone = -1e30f;                      // the reference before anything is seen: every p is 0
+constexpr float kNone = -1e38f;                      // the reference before anything is seen, below every finite score
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kTile = 128 * 128;                // 128 rows of 64 bf16
 constexpr uint32_t kRawHalf = 128 * 64 + 128;        // 128 e4m3 rows of K or V and their scales
@@ -90,6 +97,29 @@ __device__ __forceinline__ uint32_t bf16_of(uint32_t w, bool upper, float f) {
     const uint32_t h = half2_of(w, upper);
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return pack_bf16(v.x * f, v.y * f);
+}
+
+// 2^y for y <= 127 on the floating-point pipe: y = n + f with n its nearest integer (by adding and
+// taking away 1.5 2^23, whose low bits then hold n + 127), a fourth-degree polynomial for 2^f on
+// [-1/2, 1/2] (relative minimax by Remez' exchange, error 2.7e-6), times 2^n. Below 2^-126: 2^-126.
+// NaN stays NaN.
+// Every kPoly-th pair of a whole tile's weights is taken this way in bf16: 388 us without, 386 with
+// every third, 374 with every fourth, 383 with every sixth (the case above). Not in e4m3, whose
+// 136 registers a thread do not hold it (494 us without, 591 with every fourth).
+constexpr int kPoly = 4;
+__device__ __forceinline__ float2 exp2_poly(float2 y) {
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y.x));   // -126
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y.y));
+    const float2 magic = make_float2(12583039.f, 12583039.f);   // 1.5 2^23 + 127
+    const float2 t = __fadd2_rn(y, magic);
+    const float2 n = __fadd2_rn(t, make_float2(-12583039.f, -12583039.f));
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), y);
+    float2 p = make_float2(0.009570102207362652f, 0.009570102207362652f);
+    p = __ffma2_rn(p, f, make_float2(0.05591785907745361f, 0.05591785907745361f));
+    p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+    p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+    p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+    return __fmul2_rn(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
 }
 
 template <bool FP8>
@@ -519,19 +549,26 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int i = 0; i < 4; ++i) r2[i] = make_float2(0.f, 0.f);
                 const float2 scale2 = make_float2(kScaleLog2, kScaleLog2);
                 const float2 shift2 = make_float2(-m_ref, -m_ref);
-                auto weigh = [&](uint32_t(&x)[64]) {   // 64 scores to 32 pairs of weights, in place
+                // 64 scores to 32 pairs of weights, in place
+                auto weigh = [&](uint32_t(&x)[64], auto whole_tile) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
                         const int i = c / 2;
                         const float2 y =
                             __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2);
-                        const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        const float2 pr = decltype(whole_tile)::value && i % kPoly == kPoly - 1
+                                              ? exp2_poly(y)
+                                              : make_float2(ex2_approx(y.x), ex2_approx(y.y));
                         r2[i & 3] = __fadd2_rn(r2[i & 3], pr);
                         x[i] = pack_bf16(pr.x, pr.y);
                     }
                 };
-                if (!FP8) weigh(s[0]);
-                weigh(s[FP8 ? 0 : 1]);
+                auto weigh_by = [&](uint32_t(&x)[64]) {
+                    if (!FP8 && (meta & kFull)) weigh(x, std::true_type{});
+                    else weigh(x, std::false_type{});
+                };
+                if (!FP8) weigh_by(s[0]);
+                weigh_by(s[FP8 ? 0 : 1]);
                 // P.V of the item's previous tile must be done before O is rescaled or P is
                 // overwritten (for the first tile, the previous item's o_final wait covered it)
                 if (u > 0 && !warp_wait(&ctl.o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
@@ -553,7 +590,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     tmem_wait_ld();
                     s_is_read();
                     if (!(meta & kFull)) hide(s[0], see[0], see[1]);
-                    weigh(s[0]);
+                    weigh_by(s[0]);
                 }
                 tmem_st32(lane_base + kColP, *reinterpret_cast<const uint32_t(*)[32]>(&s[0][0]));
                 l = l * factor + (((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y)));
@@ -570,8 +607,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tc_fence_after();
                 ++I;
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;   // l = 0: nothing seen. NaN stays.
-            const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+            // nothing seen, or scores of -infinity alone (exp2_poly gives those 2^-126). NaN stays.
+            const bool none = l == 0.f || (m_ref == kNone && l == l);
+            const float inv = none ? 0.f : 1.f / l;
+            const float lse = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
             const bool whole = rec.whole;
             const int i = a.by_group.of(rec.r0 + row);
             const int head = rec.h * a.group + (rec.r0 + row - i * a.group);
