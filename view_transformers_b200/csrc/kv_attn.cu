@@ -796,7 +796,9 @@ static cudaError_t launch_merge(const AttnArgs& a, cudaStream_t st) {
                         st, a);
 }
 
-cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st) { return launch_merge<128>(a, st); }
+cudaError_t launch_kv_merge(const AttnArgs& a, bool wide, cudaStream_t st) {
+    return wide ? launch_merge<256>(a, st) : launch_merge<128>(a, st);
+}
 
 cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
     a.R = 1;

@@ -2,26 +2,29 @@
 // key/value head (chunks and frames), on tcgen05. The mathematics is kv_attn.cu's; the bound here
 // is the softmax: a 128 x 128 tile's exponentials (16 a clock and SM) take 1,024 clocks against
 // 650 of matrix instructions, and its other instructions share the four schedulers with them.
-// Measured: a frame of 782 new tokens, 16 heads, over 78,200 cached ones in bf16: 374 us, 670
-// TFLOP/s (767 counting the whole tiles, whose last is 11% full). With the exponentials left out
-// it took 288 us of 388 then, so the rest of a tile's chain (read S, maximum, write P, products)
-// is what stands next. 1,374 new tokens over 33 frames of 1,374 in e4m3: 494 us, 516 TFLOP/s.
+// Measured, 16 heads: a frame of 782 new tokens over 78,200 cached ones in bf16: 371 us, 675
+// TFLOP/s (773 counting the whole tiles, whose last is 11% full). With the exponentials left out
+// it took 288 us (of 388 then), so the rest of a tile's chain (read S, maximum, write P, products)
+// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 458 us, 557 TFLOP/s.
 //
-// A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA
-// warp (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O in
-// [192,256)), four softmax warps with one query row per thread, two blocks per SM; persistent,
-// the barriers running on across items as in frame_attn.cu. What differs:
-//   - a query tile is the `group` heads of 128 / group tokens (mr rows), one 3D TMA box;
+// A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA warp
+// per query tile (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O
+// in [192,256)), four softmax warps per query tile with one query row per thread; persistent, the
+// barriers running on across items as in frame_attn.cu. What differs:
+//   - a query tile is the `group` heads of 128 / group tokens, one 3D TMA box;
 //   - a 128-key tile is gathered from its pages by up to eight TMA boxes of whole pages; pages
 //     that do not exist are not loaded, and the tile's page mask (a bit per 16 keys) goes to the
 //     softmax with the stage;
-//   - tiles that not every row of the tile sees whole are taken key by key from a 128-bit mask
+//   - tiles that not every row of the block sees whole are taken key by key from a 128-bit mask
 //     per row. Their rows of V that no row sees are zeroed before the product, and NaN or
 //     infinite values that only some rows see are taken out of V and marked in the rows that do;
-//   - an e4m3 cache is copied raw into a ring of half tiles (K, V, K, ...) and four further warps
-//     turn it into the bf16 tiles that the MMA reads (exact: power-of-two scales), on the same
-//     schedulers as the softmax;
-//   - the R blocks of a team walk the same keys for R neighbouring query tiles, so that a
+//   - bf16: one query tile a block, two blocks per SM. e4m3: two query tiles a block, one block per
+//     SM. Its codes are copied raw into a ring of half tiles (K, V, K, ...) and four further warps turn
+//     them into the bf16 tiles that both products read (exact: power-of-two scales). They convert a
+//     tile once for 256 rows, and leave the registers for whole rows of scores (two blocks of one
+//     tile each measured 494 against 458 us). The schedulers fetch all roles' code, so the
+//     conversion's loop is kept short (unrolled four times: 546 against 488 us);
+//   - the R blocks of a team walk the same keys for R neighbouring pieces of a chunk, so that a
 //     key/value tile comes from HBM once for all of them; the runs of teams are as in kv_cache.cuh.
 // Every wait is bounded; a timeout is reported through the status word.
 #include <cuda.h>
@@ -38,39 +41,49 @@ namespace {
 using namespace sm100;
 using namespace kv;
 
-constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;
+constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;   // of a query tile
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
 constexpr float kNone = -1e38f;                      // the reference before anything is seen, below every finite score
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kTile = 128 * 128;                // 128 rows of 64 bf16
 constexpr uint32_t kRawHalf = 128 * 64 + 128;        // 128 e4m3 rows of K or V and their scales
-constexpr int kRaw = 3;                              // raw half tiles in flight
+constexpr int kRaw = 6;                              // raw half tiles in flight
+constexpr int kAlone = 0x1000;                       // word of a key tile: the second query tile has no rows
 constexpr uint64_t kDrainNs = 50000000ull;
 
 template <bool FP8>
 struct Cfg {
-    static constexpr int NS = FP8 ? 2 : 3;           // K/V stages
-    // warps 0 .. 3: producer, products; 4 .. 7: softmax; 8 .. 11: e4m3 conversion. Registers a thread
-    // of each four, together what the block is launched with (128 and 80 a thread)
-    static constexpr int kThreads = FP8 ? 384 : 256;
+    static constexpr int T = FP8 ? 2 : 1;            // query tiles of a block
+    static constexpr int NS = 3;                     // K/V stages
+    // Every kPoly-th pair of a whole tile's weights is taken by exp2_poly. The frame chunk above: 388 us
+    // without, 386 with every third, 374 with every fourth, 383 with every sixth; the window in e4m3, whose
+    // schedulers also convert: 475 us without, 472 with every sixth, 465 with every eighth
+    static constexpr int kPoly = FP8 ? 8 : 4;
+    // warps 0 .. 3: producer, products; 4 T softmax warps; in e4m3 four for the conversion
+    static constexpr int kThreads = FP8 ? 512 : 256;
     static constexpr uint32_t kOffQ = 0;
-    static constexpr uint32_t kOffK = kTile;
+    static constexpr uint32_t kOffK = kOffQ + T * kTile;
     static constexpr uint32_t kOffV = kOffK + NS * kTile;
     static constexpr uint32_t kOffRaw = kOffV + NS * kTile;
-    static constexpr uint32_t kOffCtl = kOffRaw + (FP8 ? kRaw * kRawHalf : 0);
+    static constexpr uint32_t kOffList = kOffRaw + (FP8 ? kRaw * kRawHalf : 0);   // [NS][128] uint2
+    static constexpr uint32_t kOffCtl = kOffList + (FP8 ? NS * 1024 : 0);
 };
 
 struct Ctl {
     uint64_t q_full, q_empty;
     uint64_t k_full[3], kv_empty[3], v_full[3];      // v_full: e4m3 only (bf16: with k_full)
+    uint64_t clean[3];                               // of a stage's V, by the first query tile's warps (two tiles)
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t rec_full[2], rec_empty[2], meet;
-    uint64_t s_full, s_free, p_full, o_done, o_final, drain;
+    struct {
+        uint64_t s_full, s_free, p_full, o_done, o_final;
+    } q[2];                                          // of the query tiles
+    uint64_t drain;
     Rec rec[2];
     int meta[3], tile[3];                            // of the stages
+    int found[3];                                    // of the stages: the last tile with values taken out, plus 1
     int raw_meta[kRaw], raw_tile[kRaw];
-    int found[2];                                    // the last even, odd tile with values taken out, plus 1
     uint32_t tmem_base;
     int abort;
     Start start;
@@ -92,21 +105,18 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {   // two 
     return r;
 }
 // two e4m3 codes times a power of two, exact, through f16 and f32: half of the instructions go to
-// the floating-point pipe (moving the bits with integer instructions alone measured slower)
+// the floating-point pipes (moving the bits with integer instructions alone measured slower)
 __device__ __forceinline__ uint32_t bf16_of(uint32_t w, bool upper, float f) {
     const uint32_t h = half2_of(w, upper);
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_bf16(v.x * f, v.y * f);
+    const float2 r = __fmul2_rn(v, make_float2(f, f));
+    return pack_bf16(r.x, r.y);
 }
 
 // 2^y for y <= 127 on the floating-point pipe: y = n + f with n its nearest integer (by adding and
 // taking away 1.5 2^23, whose low bits then hold n + 127), a fourth-degree polynomial for 2^f on
 // [-1/2, 1/2] (relative minimax by Remez' exchange, error 2.7e-6), times 2^n. Below 2^-126: 2^-126.
 // NaN stays NaN.
-// Every kPoly-th pair of a whole tile's weights is taken this way in bf16: 388 us without, 386 with
-// every third, 374 with every fourth, 383 with every sixth (the case above). Not in e4m3, whose
-// 136 registers a thread do not hold it (494 us without, 591 with every fourth).
-constexpr int kPoly = 4;
 __device__ __forceinline__ float2 exp2_poly(float2 y) {
     asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y.x));   // -126
     asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(y.y));
@@ -123,12 +133,11 @@ __device__ __forceinline__ float2 exp2_poly(float2 y) {
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(Cfg<FP8>::kThreads, 2)
+__global__ void __launch_bounds__(Cfg<FP8>::kThreads, FP8 ? 1 : 2)
 kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v,
-               const __grid_constant__ AttnArgs a) {
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a) {
     using C = Cfg<FP8>;
-    constexpr int NS = C::NS;
+    constexpr int NS = C::NS, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctl& ctl = *reinterpret_cast<Ctl*>(smem + C::kOffCtl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -148,11 +157,13 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     if (team >= start.teams || start.total == 0) return;
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 1);
-        mbar_init(&ctl.q_empty, 1);
+        mbar_init(&ctl.q_empty, T);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&ctl.k_full[s], FP8 ? 4 : 1);
             mbar_init(&ctl.v_full[s], 4);
-            mbar_init(&ctl.kv_empty[s], 1);
+            mbar_init(&ctl.kv_empty[s], T);
+            mbar_init(&ctl.clean[s], 4);
+            ctl.found[s] = 0;
         }
         for (int s = 0; s < kRaw; ++s) {
             mbar_init(&ctl.raw_full[s], 1);
@@ -160,16 +171,17 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl.rec_full[s], 1);
-            mbar_init(&ctl.rec_empty[s], 4);
+            mbar_init(&ctl.rec_empty[s], 4 * T);
         }
-        mbar_init(&ctl.s_full, 1);
-        mbar_init(&ctl.s_free, 4);
-        mbar_init(&ctl.p_full, 4);
-        mbar_init(&ctl.o_done, 1);
-        mbar_init(&ctl.o_final, 1);
-        mbar_init(&ctl.drain, 1);
+        for (int s = 0; s < T; ++s) {
+            mbar_init(&ctl.q[s].s_full, 1);
+            mbar_init(&ctl.q[s].s_free, 4);
+            mbar_init(&ctl.q[s].p_full, 4);
+            mbar_init(&ctl.q[s].o_done, 1);
+            mbar_init(&ctl.q[s].o_final, 1);
+        }
+        mbar_init(&ctl.drain, T);
         mbar_init(&ctl.meet, 4);
-        ctl.found[0] = ctl.found[1] = 0;
         ctl.abort = 0;
         fence_mbar_init();
     }
@@ -181,7 +193,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
     }
     if (warp == 1) {
-        tmem_alloc(&ctl.tmem_base, kTmemCols);
+        tmem_alloc(&ctl.tmem_base, T * kTmemCols);
         tmem_relinquish();
     }
     fence_async_shared();   // the plan's tables lay where TMA writes next
@@ -191,20 +203,25 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     int issued = 0;         // K/V tiles (e4m3: half tiles) whose loads the producer issued
     int q_loads = 0;        // Q tiles the producer issued
 
-    // Roles 0 (producer) and 1 (products) of warps 0 .. 3, 4: softmax, 5: conversion. A warp's scheduler
-    // is its number modulo 4, for the softmax's four too, so the two blocks of an SM (told apart by
-    // where their tensor memory lies) take the roles in opposite halves: no row quarter of a tile
-    // then trails the others.
-    const int role = warp >= 8 ? 5 : warp >= 4 ? 4 : tmem & 0xffffu ? warp ^ 2 : warp;
+    // Roles 0 (producer), 1 and 2 (products of the first and second query tile) of warps 0 .. 3, 4:
+    // softmax, 5: conversion. A warp's scheduler is its number modulo 4, for the softmax's too, so two
+    // blocks of an SM (told apart by where their tensor memory lies) take the roles in opposite
+    // halves: no row quarter of a tile then trails the others.
+    const int role = warp >= 4 + 4 * T ? 5 : warp >= 4 ? 4 : T == 1 && (tmem & 0xffffu) ? warp ^ 2 : warp;
+    const int tile_rows = a.mr / T;   // a query tile's
 
+    // registers a thread: together what the block is launched with (128 a thread). bf16 80 and 176: 375
+    // instead of 371 us; e4m3 72 and 184: 477 instead of 472
     if (role < 4) {
-        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (role == 0) {
             // ======================================================== producer
-            int U = 0, I = 0, X = 0;     // tiles, Q tiles, segments so far
+            int U = 0, I = 0, X = 0;     // tiles, Q loads, segments so far
+            int alone = 0;               // kAlone if the segment has no rows for the second query tile
             auto put_record = [&](const Rec& r) -> bool {
                 const int slot = X & 1;
+                alone = r.nrows <= tile_rows ? kAlone : 0;
                 if (X >= 2 && !warp_wait(&ctl.rec_empty[slot], ((X >> 1) - 1) & 1, abort, a.status)) return false;
                 if (lane == 0) {
                     ctl.rec[slot] = r;
@@ -216,13 +233,17 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             auto begin = [&](const Walk& w, int r0) -> bool {
                 if (I > 0 && !warp_wait(&ctl.q_empty, (I - 1) & 1, abort, a.status)) return false;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&ctl.q_full, a.mr * 128);
-                    tma_load_3d(smem + C::kOffQ, &tm_q, &ctl.q_full, 0, w.h * a.group, w.q.row0 + r0 / a.group);
+                    const int loads = T == 1 || alone ? 1 : 2;
+                    mbar_arrive_expect_tx(&ctl.q_full, loads * tile_rows * 128);
+                    for (int i = 0; i < loads; ++i)
+                        tma_load_3d(smem + C::kOffQ + i * kTile, &tm_q, &ctl.q_full, 0, w.h * a.group,
+                                    w.q.row0 + (r0 + i * tile_rows) / a.group);
                 }
                 q_loads = ++I;
                 return true;
             };
-            auto put_tile = [&](int meta, int t, int boxes, int rows, int at) -> bool {
+            auto put_tile = [&](int words, int t, int boxes, int rows, int at) -> bool {
+                const int meta = words | alone;
                 const int box = kUnit / boxes, i = lane - at;   // this lane's box
                 const int row = i >= 0 && i < boxes ? rows : -1, k = i * box;
                 const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
@@ -284,39 +305,52 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     put_record(rec);
                 }
             }
-        } else if (role == 1) {
-            // ======================================================== MMA issuer
+        } else if (role <= T) {
+            // ======================================================== MMA issuer of query tile g
             // The whole warp runs the loop, so that addresses and descriptors are uniform values, and one
             // lane issues. (With one lane in the loop, issuing a tile's ten products and commits took
             // 1,100 clocks, and this thread, not the exponentials, set the pace.)
             const bool leader = elect_one();
+            const int g = T == 1 ? 0 : role - 1;
+            const uint32_t tm = tmem + g * kTmemCols;
             constexpr uint32_t idesc_qk = idesc_f16(128, 128, 1u, false);
             constexpr uint32_t idesc_pv = idesc_f16(128, 64, 1u, true);
-            const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(smem + C::kOffQ + g * kTile), 16, 1024);
             const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
             const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::kOffV), 0, 1024);
             auto issue_qk = [&](int st) {
                 if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)   // 32 bytes a step, in 16-byte units
-                        mma_ss(tmem + kColS, q_desc + 2 * ks, k_desc + (uint64_t)(st * (kTile >> 4)) + 2 * ks, idesc_qk,
+                        mma_ss(tm + kColS, q_desc + 2 * ks, k_desc + (uint64_t)(st * (kTile >> 4)) + 2 * ks, idesc_qk,
                                ks > 0 ? 1u : 0u);
-                    mma_commit(&ctl.s_full);
+                    mma_commit(&ctl.q[g].s_full);
                 }
                 __syncwarp();
             };
-            int I = 0, meta = 0, st = 0;
+            int I = 0, U = 0, meta = 0, st = 0;   // segments, tiles of this query tile
             uint32_t turn = 0u;            // parity of the stage's use
-            bool fresh = true;             // tile U starts a segment
-            for (int U = 0;; ++U) {
+            bool fresh = true;             // the next tile starts a segment
+            for (;;) {
                 if (fresh) {               // within a segment its QK^T is issued already
                     if (!warp_wait(&ctl.k_full[st], turn, abort, a.status)) break;
                     meta = *(volatile int*)&ctl.meta[st];
                     if (meta & kEnd) break;
+                    if (g == 1 && (meta & kAlone)) {
+                        __syncwarp();
+                        if (leader) {
+                            mbar_arrive(&ctl.kv_empty[st]);
+                            if (meta & kLast) mbar_arrive(&ctl.q_empty);
+                        }
+                        if (meta & kLast) ++I;
+                        turn ^= st + 1 == NS ? 1u : 0u;
+                        st = st + 1 == NS ? 0 : st + 1;
+                        continue;
+                    }
                     if (!warp_wait(&ctl.q_full, I & 1, abort, a.status)) break;
                     ++I;
                     // the previous segment's last S has been read by the softmax
-                    if (U > 0 && !warp_wait(&ctl.s_free, (U - 1) & 1, abort, a.status)) break;
+                    if (U > 0 && !warp_wait(&ctl.q[g].s_free, (U - 1) & 1, abort, a.status)) break;
                     tc_fence_after();
                     issue_qk(st);
                 }
@@ -326,7 +360,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 fresh = (cur & kLast) != 0;
                 if (!fresh) {
                     if (!warp_wait(&ctl.k_full[sn], tn, abort, a.status) ||
-                        !warp_wait(&ctl.s_free, U & 1, abort, a.status))
+                        !warp_wait(&ctl.q[g].s_free, U & 1, abort, a.status))
                         break;
                     tc_fence_after();
                     issue_qk(sn);
@@ -335,18 +369,19 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     mma_commit(&ctl.q_empty);   // the segment's last Q K^T is issued
                 }
                 if (FP8 && !warp_wait(&ctl.v_full[st], turn, abort, a.status)) break;
-                if (!warp_wait(&ctl.p_full, U & 1, abort, a.status)) break;
+                if (!warp_wait(&ctl.q[g].p_full, U & 1, abort, a.status)) break;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)   // 16 rows of 128 bytes a step
-                        mma_ts(tmem + kColO, tmem + kColP + 8 * ks, v_desc + (uint64_t)(st * (kTile >> 4)) + 128 * ks, idesc_pv,
+                        mma_ts(tm + kColO, tm + kColP + 8 * ks, v_desc + (uint64_t)(st * (kTile >> 4)) + 128 * ks, idesc_pv,
                                (!(cur & kFirst) || ks > 0) ? 1u : 0u);
                     mma_commit(&ctl.kv_empty[st]);
-                    mma_commit(&ctl.o_done);
-                    if (fresh) mma_commit(&ctl.o_final);
+                    mma_commit(&ctl.q[g].o_done);
+                    if (fresh) mma_commit(&ctl.q[g].o_final);
                 }
                 __syncwarp();
+                ++U;
                 st = sn;
                 turn = tn;
             }
@@ -355,8 +390,8 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         // ============================================================ e4m3 -> bf16
         // four lanes share a row of 64 codes; each writes two 16-byte chunks of the swizzled
         // bf16 row. Rows of pages that do not exist are left as they are.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        const int cw = warp - 8;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        const int cw = warp - 4 - 4 * T;
         bool ok = true;
         for (int U = 0; ok; ++U) {
             const int st = U % NS;
@@ -381,7 +416,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     ok = false;
                     break;
                 }
-#pragma unroll 4
+#pragma unroll 1      // a short loop: see above
                 for (int i = 0; i < 4; ++i) {
                     const int r = i * 32 + cw * 8 + (lane >> 2);
                     if ((meta >> (r >> 4)) & 1) {
@@ -407,13 +442,13 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
     } else {
         // ============================================================ softmax + epilogue
-        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        const int quad = warp & 3;
+        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int quad = warp & 3, g = T == 1 ? 0 : (warp >> 2) - 1;   // g: the query tile
         const int row = quad * 32 + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        int U = 0, I = 0, met = 0;
-        auto meet = [&]() -> bool {   // the four warps; bounded like every wait
+        const uint32_t lane_base = tmem + g * kTmemCols + ((uint32_t)(quad * 32) << 16);
+        int U = 0, N = 0, I = 0, met = 0;                    // N: tiles of the block, U, I: of this query tile
+        auto meet = [&]() -> bool {   // the first query tile's four warps; bounded like every wait
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.meet);
             return warp_wait(&ctl.meet, met++ & 1, abort, a.status);
@@ -423,109 +458,92 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const Rec& rec = ctl.rec[X & 1];
             const int tiles = rec.tiles;
             if (tiles < 0) break;
+            const int nrows = min(tile_rows, rec.nrows - g * tile_rows), r0 = rec.r0 + g * tile_rows;
+            if (nrows <= 0) {         // the products skip these tiles too
+                N += tiles;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.rec_empty[X & 1]);
+                continue;
+            }
             float m_ref = kNone, l = 0.f;
             uint32_t poison0 = 0u, poison1 = 0u;   // columns that met a non-finite value of a key the row sees
             int lo = 0, hi = 0;
-            if (row < rec.nrows) visible(a, rec.len, rec.pos0 + a.by_group.of(rec.r0 + row), lo, hi);
+            if (row < nrows) visible(a, rec.len, rec.pos0 + a.by_group.of(r0 + row), lo, hi);
             bool ok = true;
-            for (int u = 0; u < tiles; ++u, ++U) {
-                const int st = U % NS;
-                if (!warp_wait(&ctl.s_full, U & 1, abort, a.status)) { ok = false; break; }
+            for (int u = 0; u < tiles; ++u, ++U, ++N) {
+                const int st = N % NS;
+                if (!warp_wait(&ctl.q[g].s_full, U & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
-                // bf16: S in 128 registers. e4m3: half of it at a time, the first half read again for its
-                // exponentials, so that 136 registers a thread do and four warps can convert.
-                uint32_t s[FP8 ? 1 : 2][64];
-                auto load = [&](uint32_t(&x)[64], int c0) {
-                    tmem_ld32(lane_base + kColS + c0, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                    tmem_ld32(lane_base + kColS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                };
-                auto s_is_read = [&] {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.s_free);
-                };
-                auto top_of = [&](const uint32_t(&x)[64]) {
-                    float acc[4];
+                uint32_t s[128];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = __uint_as_float(x[i]);
-#pragma unroll
-                    for (int c = 4; c < 64; c += 2)
-                        acc[(c / 2) & 3] = max3f(acc[(c / 2) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                    return fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3]));
-                };
-                auto hide = [&](uint32_t(&x)[64], uint32_t see0, uint32_t see1) {   // what the row does not see
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (!(((c < 32 ? see0 : see1) >> (c & 31)) & 1u)) x[c] = 0xff800000u;   // -infinity
-                };
-                load(s[0], 0);
-                if (!FP8) load(s[FP8 ? 0 : 1], 64);
+                for (int k = 0; k < 4; ++k)
+                    tmem_ld32(lane_base + kColS + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * k]));
                 // the tile's words: written before k_full, for which the product's thread waited
                 const int meta = *(volatile int*)&ctl.meta[st];
                 tmem_wait_ld();
-                if (!FP8) s_is_read();
-                float mt;
-                uint32_t see[4];
-                if (meta & kFull) {
-                    mt = top_of(s[0]);
-                    if (FP8) {
-                        load(s[0], 64);
-                        tmem_wait_ld();
-                    }
-                    mt = fmaxf(mt, top_of(s[FP8 ? 0 : 1]));
-                } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.q[g].s_free);
+                if (!(meta & kFull)) {
                     // columns of this row that count
                     const int k0 = ctl.tile[st] * kUnit;
+                    uint32_t see[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int b = k0 + 32 * k;
                         see[k] = low_bits(hi - b) & (~low_bits(lo - b) | low_bits(a.sink - b)) &
                                  (((meta >> (2 * k)) & 1 ? 0xffffu : 0u) | ((meta >> (2 * k + 1)) & 1 ? 0xffff0000u : 0u));
                     }
-                    hide(s[0], see[0], see[1]);
-                    mt = top_of(s[0]);
-                    if (FP8) {
-                        load(s[0], 64);
-                        tmem_wait_ld();
-                    }
-                    hide(s[FP8 ? 0 : 1], see[2], see[3]);
-                    mt = fmaxf(mt, top_of(s[FP8 ? 0 : 1]));
-                    // V of key k0 + row: P = 0 does not silence what is not finite
-                    if (FP8 && !warp_wait(&ctl.v_full[st], (U / NS) & 1, abort, a.status)) { ok = false; break; }
-                    uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * kTile + row * 128);
-                    const int key = k0 + row;
-                    const bool any = ((meta >> (row >> 4)) & 1) && key < rec.hi_max && (key >= rec.lo_min || key < a.sink);
-                    uint32_t bad0 = 0u, bad1 = 0u;
-                    if (any) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (!((see[c / 32] >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -infinity
+                    // What was taken out of each row of V. One query tile: rare, and K's tile is done with (S
+                    // is there), so its memory passes it on.
+                    uint2* list = reinterpret_cast<uint2*>(T == 2 ? smem + C::kOffList + st * 1024
+                                                                  : smem + C::kOffK + st * kTile);
+                    if (g == 0) {
+                        // V of key k0 + row: P = 0 does not silence what is not finite
+                        if (FP8 && !warp_wait(&ctl.v_full[st], (N / NS) & 1, abort, a.status)) { ok = false; break; }
+                        uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * kTile + row * 128);
+                        const int key = k0 + row;
+                        const bool any =
+                            ((meta >> (row >> 4)) & 1) && key < rec.hi_max && (key >= rec.lo_min || key < a.sink);
+                        uint32_t bad0 = 0u, bad1 = 0u;
+                        if (any) {
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 x = v[c];
-                            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t bits = 0u, z[4];
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 x = v[c];
+                                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                                uint32_t bits = 0u, z[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const bool b0 = (y[i] & 0x7f80u) == 0x7f80u, b1 = (y[i] & 0x7f800000u) == 0x7f800000u;
-                                z[i] = (b0 ? 0u : y[i] & 0xffffu) | (b1 ? 0u : y[i] & 0xffff0000u);
-                                bits |= (b0 ? 1u : 0u) << (2 * i) | (b1 ? 2u : 0u) << (2 * i);
+                                for (int i = 0; i < 4; ++i) {
+                                    const bool b0 = (y[i] & 0x7f80u) == 0x7f80u, b1 = (y[i] & 0x7f800000u) == 0x7f800000u;
+                                    z[i] = (b0 ? 0u : y[i] & 0xffffu) | (b1 ? 0u : y[i] & 0xffff0000u);
+                                    bits |= (b0 ? 1u : 0u) << (2 * i) | (b1 ? 2u : 0u) << (2 * i);
+                                }
+                                if (bits) {
+                                    v[c] = make_uint4(z[0], z[1], z[2], z[3]);
+                                    const int col = ((c ^ (row & 7)) & 7) * 8;   // the chunk's first column
+                                    if (col < 32) bad0 |= bits << col;
+                                    else bad1 |= bits << (col - 32);
+                                }
                             }
-                            if (bits) {
-                                v[c] = make_uint4(z[0], z[1], z[2], z[3]);
-                                const int col = ((c ^ (row & 7)) & 7) * 8;   // the chunk's first column
-                                if (col < 32) bad0 |= bits << col;
-                                else bad1 |= bits << (col - 32);
-                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    // rare: K's tile is done with (S is there), so its memory passes the columns on
-                    if (bad0 | bad1) ctl.found[U & 1] = U + 1;
-                    if (!meet()) { ok = false; break; }
-                    if (*(volatile int*)&ctl.found[U & 1] == U + 1) {
-                        uint2* list = reinterpret_cast<uint2*>(smem + C::kOffK + st * kTile);
-                        list[row] = make_uint2(bad0, bad1);
+                        if (bad0 | bad1) ctl.found[st] = N + 1;
                         if (!meet()) { ok = false; break; }
+                        if (*(volatile int*)&ctl.found[st] == N + 1) {
+                            list[row] = make_uint2(bad0, bad1);
+                            if (!meet()) { ok = false; break; }
+                        }
+                        fence_async_shared();
+                    } else if (!warp_wait(&ctl.clean[st], (N / NS) & 1, abort, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (*(volatile int*)&ctl.found[st] == N + 1) {
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k)
 #pragma unroll 1
@@ -535,8 +553,22 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                     poison0 |= b.x;
                                     poison1 |= b.y;
                                 }
+                        if (T == 1) fence_async_shared();
                     }
-                    fence_async_shared();
+                }
+                if (T == 2 && g == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.clean[st]);
+                }
+                float mt;
+                {
+                    float acc[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] = __uint_as_float(s[i]);
+#pragma unroll
+                    for (int c = 4; c < 128; c += 2)
+                        acc[(c / 2) & 3] = max3f(acc[(c / 2) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                    mt = fmaxf(fmaxf(acc[0], acc[1]), fmaxf(acc[2], acc[3]));
                 }
                 const float mt2 = mt * kScaleLog2;
                 const bool need = mt2 > m_ref + kRescale;
@@ -549,29 +581,25 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int i = 0; i < 4; ++i) r2[i] = make_float2(0.f, 0.f);
                 const float2 scale2 = make_float2(kScaleLog2, kScaleLog2);
                 const float2 shift2 = make_float2(-m_ref, -m_ref);
-                // 64 scores to 32 pairs of weights, in place
-                auto weigh = [&](uint32_t(&x)[64], auto whole_tile) {
+                // 128 scores to 64 pairs of weights, in place
+                auto weigh = [&](auto whole_tile) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
+                    for (int c = 0; c < 128; c += 2) {
                         const int i = c / 2;
                         const float2 y =
-                            __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2);
-                        const float2 pr = decltype(whole_tile)::value && i % kPoly == kPoly - 1
+                            __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, shift2);
+                        const float2 pr = decltype(whole_tile)::value && i % C::kPoly == C::kPoly - 1
                                               ? exp2_poly(y)
                                               : make_float2(ex2_approx(y.x), ex2_approx(y.y));
                         r2[i & 3] = __fadd2_rn(r2[i & 3], pr);
-                        x[i] = pack_bf16(pr.x, pr.y);
+                        s[i] = pack_bf16(pr.x, pr.y);
                     }
                 };
-                auto weigh_by = [&](uint32_t(&x)[64]) {
-                    if (!FP8 && (meta & kFull)) weigh(x, std::true_type{});
-                    else weigh(x, std::false_type{});
-                };
-                if (!FP8) weigh_by(s[0]);
-                weigh_by(s[FP8 ? 0 : 1]);
+                if (meta & kFull) weigh(std::true_type{});
+                else weigh(std::false_type{});
                 // P.V of the item's previous tile must be done before O is rescaled or P is
                 // overwritten (for the first tile, the previous item's o_final wait covered it)
-                if (u > 0 && !warp_wait(&ctl.o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
+                if (u > 0 && !warp_wait(&ctl.q[g].o_done, (U - 1) & 1, abort, a.status)) { ok = false; break; }
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, corr)) {
 #pragma unroll
@@ -584,26 +612,20 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         tmem_st32(lane_base + kColO + 32 * k, o);
                     }
                 }
-                tmem_st32(lane_base + kColP + 32, *reinterpret_cast<const uint32_t(*)[32]>(&s[FP8 ? 0 : 1][0]));
-                if (FP8) {
-                    load(s[0], 0);
-                    tmem_wait_ld();
-                    s_is_read();
-                    if (!(meta & kFull)) hide(s[0], see[0], see[1]);
-                    weigh_by(s[0]);
-                }
-                tmem_st32(lane_base + kColP, *reinterpret_cast<const uint32_t(*)[32]>(&s[0][0]));
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    tmem_st32(lane_base + kColP + 32 * k, *reinterpret_cast<const uint32_t(*)[32]>(&s[32 * k]));
                 l = l * factor + (((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y)));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_full);
+                if (lane == 0) mbar_arrive(&ctl.q[g].p_full);
             }
             if (!ok) break;
             // -------------------------------------------------------- epilogue of the segment
             const bool some = tiles > 0;
             if (some) {
-                if (!warp_wait(&ctl.o_final, I & 1, abort, a.status)) break;
+                if (!warp_wait(&ctl.q[g].o_final, I & 1, abort, a.status)) break;
                 tc_fence_after();
                 ++I;
             }
@@ -612,9 +634,10 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const float inv = none ? 0.f : 1.f / l;
             const float lse = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
             const bool whole = rec.whole;
-            const int i = a.by_group.of(rec.r0 + row);
-            const int head = rec.h * a.group + (rec.r0 + row - i * a.group);
-            float* part = part_at<128>(a, team, rec.run, member);
+            const int i = a.by_group.of(r0 + row);
+            const int head = rec.h * a.group + (r0 + row - i * a.group);
+            float* part = part_at<128 * T>(a, team, rec.run, member);
+            const int at = g * tile_rows + row;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float o[32];
@@ -632,20 +655,20 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                     for (int c = 0; c < 32; ++c) o[c] = 0.f;
                 }
-                if (row < rec.nrows) {
+                if (row < nrows) {
                     if (whole) {
                         __nv_bfloat16* dst = a.out + (long long)(rec.row0 + i) * a.out_stride + head * 64 + 32 * k;
 #pragma unroll
                         for (int c = 0; c < 32; c += 8) Vec16<__nv_bfloat16>::store(dst + c, o + c);
                     } else {
-                        float* dst = part + row * 64 + 32 * k;
+                        float* dst = part + at * 64 + 32 * k;
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) Vec16<float>::store(dst + c, o + c);
                     }
                 }
             }
-            if (row < rec.nrows) {
-                if (!whole) part[128 * 64 + row] = lse;
+            if (row < nrows) {
+                if (!whole) part[T * 128 * 64 + at] = lse;
                 else if (a.lse != nullptr) a.lse[(long long)head * a.rows + rec.row0 + i] = lse;
             }
             tc_fence_before();
@@ -664,7 +687,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int u = max(0, issued - ring); u < issued; ++u)
                 mbar_wait(FP8 ? &ctl.raw_full[u % ring] : &ctl.k_full[u % ring], (u / ring) & 1, &never, a.status, kDrainNs);
         }
-        if (role == 1 && elect_one()) {   // the thread that issued the products
+        if (role >= 1 && role <= T && elect_one()) {   // the threads that issued the products
             mma_commit(&ctl.drain);
             mbar_wait(&ctl.drain, 0, &never, a.status, kDrainNs);
         }
@@ -672,7 +695,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, T * kTmemCols);
     }
 }
 
@@ -688,7 +711,7 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, cons
 
 }  // namespace
 
-cudaError_t launch_kv_merge(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv_merge(const AttnArgs& a, bool wide, cudaStream_t st);
 
 // Blocks per team. The R blocks of a team read the same keys at about the same time, so with
 // tiles query tiles per chunk the cache comes from HBM tiles / R times instead of tiles times;
@@ -709,8 +732,10 @@ static int team_size(const AttnArgs& a, int blocks, int max_new) {
 
 cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
     const uint32_t tokens = 128 / a.group;
-    a.mr = (int)tokens * a.group;
+    const int per_block = fp8 ? Cfg<true>::T : Cfg<false>::T;
+    a.mr = (int)tokens * a.group * per_block;
     a.min_run = 2;
+    a.max_teams /= per_block;            // as many blocks per SM as keep its tensor memory full
     a.R = team_size(a, a.max_teams, max_new);
     a.max_teams /= a.R;
     a.set_divisors();
@@ -724,7 +749,7 @@ cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
         return cudaErrorInvalidValue;
     }
     const cudaError_t e = fp8 ? launch<true>(a, q, k, v, st) : launch<false>(a, q, k, v, st);
-    return e != cudaSuccess ? e : launch_kv_merge(a, st);
+    return e != cudaSuccess ? e : launch_kv_merge(a, fp8, st);
 }
 
 }  // namespace bsa
