@@ -783,7 +783,8 @@ template <bool FP8, int M>
 cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
     using C = Cfg<FP8, M>;
     auto kern = kv_rows_kernel<FP8, M>;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem, allowed);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(a.max_teams), kThreads, C::kSmem, st, a);
 }

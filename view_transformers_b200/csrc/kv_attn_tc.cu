@@ -5,7 +5,7 @@
 // Measured, 16 heads: a frame of 782 new tokens over 78,200 cached ones in bf16: 371 us, 675
 // TFLOP/s (773 counting the whole tiles, whose last is 11% full). With the exponentials left out
 // it took 288 us (of 388 then), so the rest of a tile's chain (read S, maximum, write P, products)
-// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 458 us, 557 TFLOP/s.
+// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 450 us, 566 TFLOP/s.
 //
 // A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA warp
 // per query tile (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O
@@ -22,8 +22,9 @@
 //     SM. Its codes are copied raw into a ring of half tiles (K, V, K, ...) and four further warps turn
 //     them into the bf16 tiles that both products read (exact: power-of-two scales). They convert a
 //     tile once for 256 rows, and leave the registers for whole rows of scores (two blocks of one
-//     tile each measured 494 against 458 us). The schedulers fetch all roles' code, so the
-//     conversion's loop is kept short (unrolled four times: 546 against 488 us);
+//     tile each measured 494 against 458 us, but 85 against 94 us on 15 chunks of 1 to 199 rows,
+//     most with rows for one tile alone). The schedulers fetch all roles' code, so the conversion's
+//     loop is kept short (unrolled four times: 546 us, once 488, when that was tried; twice 450 now);
 //   - the R blocks of a team walk the same keys for R neighbouring pieces of a chunk, so that a
 //     key/value tile comes from HBM once for all of them; the runs of teams are as in kv_cache.cuh.
 // Every wait is bounded; a timeout is reported through the status word.
@@ -416,7 +417,7 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     ok = false;
                     break;
                 }
-#pragma unroll 1      // a short loop: see above
+#pragma unroll 2      // a short loop: see above
                 for (int i = 0; i < 4; ++i) {
                     const int r = i * 32 + cw * 8 + (lane >> 2);
                     if ((meta >> (r >> 4)) & 1) {
@@ -704,7 +705,8 @@ cudaError_t launch(AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, cons
     using C = Cfg<FP8>;
     const size_t smem = C::kOffCtl + (sizeof(Ctl) + 15) / 16 * 16;
     auto kern = kv_tc_kernel<FP8>;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(a.max_teams * a.R), C::kThreads, smem, st, q, k, v, a);
 }
@@ -718,7 +720,7 @@ cudaError_t launch_kv_merge(const AttnArgs& a, bool wide, cudaStream_t st);
 // against that stand the members without a tile in a chunk's last row group and the blocks left
 // over when R does not divide their number. The largest R within 4% of the best use of the
 // blocks; 1 for chunks of unequal lengths (max_new well above the mean), whose short ones would
-// leave members idle.
+// leave members idle. The frame chunk above: R = 7 388 us, R = 1 432 us (of 388 then).
 static int team_size(const AttnArgs& a, int blocks, int max_new) {
     const int tiles = (int)(((long long)max_new * a.group + a.mr - 1) / a.mr);
     if (tiles < 2 || (long long)a.rows * 100 < (long long)a.c.seqs * max_new * 85) return 1;

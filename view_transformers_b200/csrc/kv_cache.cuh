@@ -2,9 +2,8 @@
 // token sees, and how the attention's work is split over blocks.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
-#include <mutex>
-#include <vector>
 
 #include "common.cuh"
 
@@ -301,11 +300,12 @@ static __device__ __noinline__ Start plan_many(const AttnArgs& a, int team, int*
         bool over = false;
         for (int s0 = 0; s0 < S; s0 += 32) {
             const int per = s0 + lane < S ? pre[s0 + lane] : 0;
-            over |= (float)per * (float)a.c.kv_heads > (float)(kMostUnits / 32) || base > kMostUnits;
+            over |= (float)per * (float)a.c.kv_heads > (float)(kMostUnits / 32);
             const int own = per * a.c.kv_heads;
             const int v = lane_scan(own, lane);
             if (s0 + lane < S) pre[s0 + lane] = base + v - own;
-            base += __shfl_sync(0xffffffffu, v, 31);
+            base += __shfl_sync(0xffffffffu, v, 31);   // at most 2^30 + 32 * 2^25
+            over |= (uint32_t)base > (uint32_t)kMostUnits;
             if (__any_sync(0xffffffffu, over)) break;
         }
         if (__any_sync(0xffffffffu, over)) {
@@ -392,7 +392,6 @@ struct Rec {
     int row0, pos0, len;   // packed row and position of the chunk's first token, cached tokens
     int h, whole, run;     // key/value head; the segment is the whole item; run of the partial result
     int lo_min, hi_max;    // positions outside the sink that some row sees
-    int lo_max, hi_min;    // [lo_max, hi_min) is seen by every row
 };
 
 // Words of a key tile: a bit per 16 keys whose page exists, and these.
@@ -434,8 +433,6 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
         rec.run = w.has_start ? 1 : 0;
         rec.lo_min = own.lo_min;
         rec.hi_max = own.hi_max;
-        rec.lo_max = own.lo_max;
-        rec.hi_min = own.hi_min;
         if (!put_record(rec)) return false;
         if (tiles > 0 && !begin(w, r0)) return false;
         // lane i: box i % boxes of the run's tile jb + i / boxes; the next batch's page ids are on
@@ -502,22 +499,15 @@ __device__ __forceinline__ float* part_at(const AttnArgs& a, int team, int run, 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Allows a kernel its dynamic shared memory, once per kernel and device.
-inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
-    struct Done {
-        const void* kernel;
-        int device;
-    };
-    static std::mutex mutex;
-    static std::vector<Done> done;
+// Allows a kernel its dynamic shared memory, once per device (`done`: a bit each, of the first 64).
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const std::lock_guard<std::mutex> lock(mutex);
-    for (const Done& d : done)
-        if (d.kernel == kernel && d.device == dev) return cudaSuccess;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done.push_back({kernel, dev});
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 
