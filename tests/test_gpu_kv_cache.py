@@ -510,3 +510,118 @@ def test_a_stream_of_frames_through_the_attention_block(fmt):
     lay = oracle.Layout(frames, T, 5, H, D, w.block)
     want = oracle.layer_forward(q.double().cpu().numpy(), np.concatenate(K), np.concatenate(V), lay, L.selected())
     assert rel_l2(out, want) <= 2e-3
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [1, 3])
+def test_pieces_of_every_size_beside_one_another(fmt, group):
+    """Chunks around the borders of query tiles (128 / group tokens) and pairs of them, in one call; sequences that
+    end inside a page; windows and a sink; the same call under three bounds max_new."""
+    import torch
+    t = 128 // group
+    new = (1, t - 1, 0, t, t + 1, 2 * t - 1, 2 * t, 2 * t + 1, 300, 5)
+    lens = tuple(n + e for n, e in zip(new, (0, 130, 40, 1, 517, 0, 127, 256, 700, 1200)))
+    for unit, window, sink in ((0, 0, 0), (1, 0, 0), (31, 4, 70)):
+        c = Case("pieces", new, lens, heads=2 * group, kv_heads=2, page=32, fmt=fmt, unit=unit, window=window, sink=sink,
+                 evict=((1, 2), (6, 0), (8, 11)))
+        x, host = tensors(c, seed=unit)
+        want = attention_oracle(c, host)
+        for mx in (300, 17, 5000):
+            cache, out, lse = _attend(c, x, max_new=mx)
+            check_attention(out, lse, want)
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,back", [(40, 20), (300, 150), (300, 40), (300, 299)])
+def test_nan_values_inside_a_chunk(fmt, n, back):
+    """The rows from the NaN on are spoiled, in every query tile that holds some; those before are not."""
+    import torch
+    c = Case("nan", (n,), (n + 70,), heads=1, kv_heads=1, page=64, fmt=fmt, unit=1)
+    x, host = tensors(c)
+    pos = n + 70 - back                                       # seen by the chunk's last `back` rows
+    page, slot = int(x["table"][0, pos // 64]), pos % 64
+    if fmt == "bf16":
+        x["v_pool"][page, 0, slot, 33] = float("nan")
+    else:
+        x["v_scale"].view(torch.uint8)[page, 0, slot] = 255
+    _, out, lse = _attend(c, x)
+    o, l, bo, bl = attention_oracle(c, host)
+    k = n - back
+    check_attention(out[:k], lse[:, :k], (o[:k], l[:, :k], bo[:k], bl[:, :k]))
+    bad = torch.isnan(out[k:, 0].float())
+    assert bool(bad[:, 33].all())
+    if fmt == "bf16":
+        keep = [c for c in range(D) if c != 33]
+        assert not bool(bad[:, keep].any())
+        check_attention(out[k:][..., keep], lse[:, k:], (o[k:][..., keep], l[:, k:], bo[k:][..., keep], bl[:, k:]))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_many_sequences(fmt):
+    """More sequences than a warp has lanes, with few rows each and with many; the most there may be."""
+    for new, lens, unit in ((tuple(i * 7 % 90 for i in range(45)), tuple(i * 7 % 90 + i * 31 % 300 for i in range(45)), 1),
+                            (tuple(int(i % 9 == 0) for i in range(1024)), tuple(1 + i * 13 % 40 for i in range(1024)), 0)):
+        c = Case("many", new, lens, heads=2, kv_heads=1, page=16, fmt=fmt, unit=unit)
+        x, host = tensors(c)
+        cache, out, lse = _attend(c, x)
+        check_attention(out, lse, attention_oracle(c, host))
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_sequences_that_share_pages(n):
+    """A common prefix: the first pages of two sequences are the same pages."""
+    import torch
+    c = Case("prefix", (n, n), (n + 64, n + 64), heads=2, kv_heads=2, page=16, unit=1)
+    x, host = tensors(c)
+    x["table"][1, :4] = x["table"][0, :4]                     # 64 positions
+    for kv in "kv":
+        host[kv][1][:64] = host[kv][0][:64]
+    cache, out, lse = _attend(c, x)
+    check_attention(out, lse, attention_oracle(c, host))
+    assert cache.check_status() == 0
+
+
+def test_calls_without_rows():
+    import torch
+    c = Case("none", (0, 0), (5, 0))
+    x, _ = tensors(c)
+    cache = cache_over(c, x)
+    empty = torch.empty((0, 2, D), dtype=torch.bfloat16, device="cuda")
+    assert cache.attend(empty, x["cu"], 0).shape == (0, 2, D)
+    cache.append(empty, empty, x["cu"])
+    k, v = cache.read(x["cu"], torch.zeros(2, dtype=torch.int32, device="cuda"), rows=0)
+    assert k.shape == v.shape == (0, 2, D) and cache.check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_pools_beyond_32_bit_offsets(fmt):
+    """Pages whose bytes lie past 2^32: written, read back and attended over."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    P, n, m = 256, 140, 700
+    pages = (1 << 32) // (P * 64 * (2 if fmt == "bf16" else 1)) + 8
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    pools = [torch.empty((pages, 1, P, D), dtype=dtype, device="cuda") for _ in range(2)]
+    scales = [torch.empty((pages, 1, P), dtype=torch.uint8, device="cuda") for _ in range(2)] if fmt == "e4m3" else (None, None)
+    table = torch.tensor([[pages - 1, pages - 4, pages - 2]], dtype=torch.int32, device="cuda")
+    length = torch.tensor([m], dtype=torch.int32, device="cuda")
+    cache = KVCache.over(*pools, table, length, 1, *scales)
+    rng = np.random.default_rng(11)
+    host = {s: bf16(rng.standard_normal((m, 1, D))) for s in "qkv"}
+    dev = {s: torch.from_numpy(host[s]).to(torch.bfloat16).cuda() for s in "qkv"}
+    cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    cache.append(dev["k"], dev["v"], cu)
+    back = cache.read(cu, torch.zeros(1, dtype=torch.int32, device="cuda"), rows=m)
+    for got, s in zip(back, "kv"):
+        want = okv.dequantise(*okv.quantise(host[s])) if fmt == "e4m3" else host[s]
+        assert np.array_equal(got.double().cpu().numpy(), want)
+        host[s] = want
+    for k in (1, n):
+        c = Case("far", (k,), (m,), heads=1, kv_heads=1, fmt=fmt, unit=1)
+        want = attention_oracle(c, {"q": [host["q"][:k]], "k": [host["k"]], "v": [host["v"]], "gone": [np.zeros(m, bool)]})
+        lse = torch.empty((1, k), dtype=torch.float32, device="cuda")
+        out = cache.attend(dev["q"][:k], torch.tensor([0, k], dtype=torch.int32, device="cuda"), k, unit=1, lse=lse)
+        check_attention(out, lse, want)
+    assert cache.check_status() == 0
