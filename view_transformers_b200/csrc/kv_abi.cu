@@ -155,8 +155,19 @@ bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + desc_bytes());
     a.status = status_dev;
     a.max_teams = max_blocks();
+    // Query rows of a key/value head, at most, choose the kernel: up to 8 the form for few rows with 8 of
+    // the small instruction's 16 rows, up to 16 that with all 16, else the form for many. Measured
+    // (us; 8 rows, 16 rows, many), 16 heads:
+    //   bf16  1 stream of 78,200 keys, 8 rows:  74.3, 80.7, 67.3; 16 rows:  128, 82.1, 69.1; 17 rows: 183, 138, 68.3
+    //         8 streams of 1,000,      5 rows:  15.6, 19.7, 19.8; 12 rows: 22.0, 20.4, 19.9
+    //         1 stream of 1,000,       5 rows:   9.6, 11.8, 14.2; 12 rows: 10.4, 12.7, 14.3
+    //         6 chunks of 16 rows over up to 95 keys, 4 heads: 7.6 with 16 rows, 17.3 with many
+    //   e4m3  1 stream of 78,200,      8 rows:  48.3, 71.8,  109; 16 rows: 76.4, 75.5,  110; 24 rows: 105, 121, 110
+    //         32 streams of 9,000,     8 rows:   133,  212,  382; 16 rows:  250,  217,  384; 32 rows: 481, 438, 389
+    // In bf16 the form for many is up to 16% faster from 9 rows on, over long caches, but half as fast over
+    // short ones, and the lengths are on the device.
     const bool fp8 = cache->format == BSA_KV_E4M3;
-    const long long per_head = (long long)max_new * a.group;   // query rows of a key/value head, at most
+    const long long per_head = (long long)max_new * a.group;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return from_cuda(per_head > 16 ? launch_kv_tc(a, fp8, max_new, st) : launch_kv_rows(a, fp8, per_head <= 8, st));
 }
