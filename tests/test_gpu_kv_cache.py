@@ -558,6 +558,24 @@ def test_nan_values_inside_a_chunk(fmt, n, back):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 12, 40, 200])
+def test_a_nan_key_spoils_a_row_however_its_keys_are_split(n, fmt):
+    import torch
+    for m in (300, 2000, 6000):
+        c = Case("nan", (n,), (m,), heads=2, kv_heads=2, page=64, fmt=fmt, unit=0)
+        for pos in (0, m // 3, m - 1):
+            x, _ = tensors(c)
+            page, slot = int(x["table"][0, pos // 64]), pos % 64
+            if fmt == "bf16":
+                x["k_pool"][page, 1, slot, 9] = float("nan")
+            else:
+                x["k_scale"].view(torch.uint8)[page, 1, slot] = 255
+            _, out, lse = _attend(c, x)
+            assert bool(torch.isnan(out[:, 1]).all()) and bool(torch.isnan(lse[1]).all()), (m, pos)
+            assert bool(torch.isfinite(out[:, 0]).all()) and bool(torch.isfinite(lse[0]).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_many_sequences(fmt):
     """More sequences than a warp has lanes, with few rows each and with many; the most there may be."""
     for new, lens, unit in ((tuple(i * 7 % 90 for i in range(45)), tuple(i * 7 % 90 + i * 31 % 300 for i in range(45)), 1),

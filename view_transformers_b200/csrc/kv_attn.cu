@@ -762,7 +762,7 @@ kv_merge_kernel(const AttnArgs a) {
         for (int k = 1; k < sets; ++k) {
             const float2 o = sml[slot + k][c];
             const float4 v = sacc[slot + k][c];
-            if (o.x == -INFINITY) continue;
+            if (o.y == 0.f) continue;            // nothing seen (a NaN sum has no maximum either)
             const float n = fmaxf(m, o.x), f0 = ex2_approx(m - n), f1 = ex2_approx(o.x - n);
             m = n;
             sum = sum * f0 + o.y * f1;
