@@ -808,7 +808,6 @@ cudaError_t launch_kv_merge(const AttnArgs& a, bool wide, cudaStream_t st) {
 cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
     a.R = 1;
     a.mr = eight ? 8 : 16;
-    a.min_run = 1;
     a.set_divisors();
     const cudaError_t e = eight ? (fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st))
                                 : (fp8 ? launch_rows<true, 16>(a, st) : launch_rows<false, 16>(a, st));

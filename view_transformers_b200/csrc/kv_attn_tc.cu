@@ -496,8 +496,12 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                  (((meta >> (2 * k)) & 1 ? 0xffffu : 0u) | ((meta >> (2 * k + 1)) & 1 ? 0xffff0000u : 0u));
                     }
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!((see[c / 32] >> (c & 31)) & 1u)) s[c] = 0xff800000u;   // -infinity
+                    for (int k = 0; k < 4; ++k) {
+                        if (__all_sync(0xffffffffu, see[k] == 0xffffffffu)) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((see[k] >> c) & 1u)) s[32 * k + c] = 0xff800000u;   // -infinity
+                    }
                     // What was taken out of each row of V. One query tile: rare, and K's tile is done with (S
                     // is there), so its memory passes it on.
                     uint2* list = reinterpret_cast<uint2*>(T == 2 ? smem + C::kOffList + st * 1024
@@ -509,35 +513,42 @@ kv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         const int key = k0 + row;
                         const bool any =
                             ((meta >> (row >> 4)) & 1) && key < rec.hi_max && (key >= rec.lo_min || key < a.sink);
-                        uint32_t bad0 = 0u, bad1 = 0u;
-                        if (any) {
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                const uint4 x = v[c];
-                                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-                                uint32_t bits = 0u, z[4];
+                        // Keys that some rows see and others do not, if any: the rest a NaN spoils for all, or none
+                        const bool mixed = (rec.hi_min < rec.hi_max && rec.hi_min < k0 + kUnit && rec.hi_max > k0) ||
+                                           (rec.lo_min < rec.lo_max && rec.lo_min < k0 + kUnit && rec.lo_max > k0);
+                        if (!any) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const bool b0 = (y[i] & 0x7f80u) == 0x7f80u, b1 = (y[i] & 0x7f800000u) == 0x7f800000u;
-                                    z[i] = (b0 ? 0u : y[i] & 0xffffu) | (b1 ? 0u : y[i] & 0xffff0000u);
-                                    bits |= (b0 ? 1u : 0u) << (2 * i) | (b1 ? 2u : 0u) << (2 * i);
-                                }
-                                if (bits) {
-                                    v[c] = make_uint4(z[0], z[1], z[2], z[3]);
-                                    const int col = ((c ^ (row & 7)) & 7) * 8;   // the chunk's first column
-                                    if (col < 32) bad0 |= bits << col;
-                                    else bad1 |= bits << (col - 32);
+                            for (int c = 0; c < 8; ++c) v[c ^ (row & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        if (mixed) {
+                            uint32_t bad0 = 0u, bad1 = 0u;
+#pragma unroll 2
+                            for (int c = 0; c < (any ? 8 : 0); ++c) {   // columns 8 c .. 8 c + 7, swizzled
+                                uint4* at = v + (c ^ (row & 7));
+                                const uint4 x = *at;
+                                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                                uint32_t full = 0u;         // an exponent of all ones carries into the sign's place
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) full |= (y[i] & 0x7f807f80u) + 0x00800080u;
+                                if (full & 0x80008000u) {
+                                    uint32_t bits = 0u, z[4];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const bool b0 = (y[i] & 0x7f80u) == 0x7f80u, b1 = (y[i] & 0x7f800000u) == 0x7f800000u;
+                                        z[i] = (b0 ? 0u : y[i] & 0xffffu) | (b1 ? 0u : y[i] & 0xffff0000u);
+                                        bits |= (b0 ? 1u : 0u) << (2 * i) | (b1 ? 2u : 0u) << (2 * i);
+                                    }
+                                    *at = make_uint4(z[0], z[1], z[2], z[3]);
+                                    if (c < 4) bad0 |= bits << (8 * c);
+                                    else bad1 |= bits << (8 * c - 32);
                                 }
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        if (bad0 | bad1) ctl.found[st] = N + 1;
-                        if (!meet()) { ok = false; break; }
-                        if (*(volatile int*)&ctl.found[st] == N + 1) {
-                            list[row] = make_uint2(bad0, bad1);
+                            if (bad0 | bad1) ctl.found[st] = N + 1;
                             if (!meet()) { ok = false; break; }
+                            if (*(volatile int*)&ctl.found[st] == N + 1) {
+                                list[row] = make_uint2(bad0, bad1);
+                                if (!meet()) { ok = false; break; }
+                            }
                         }
                         fence_async_shared();
                     } else if (!warp_wait(&ctl.clean[st], (N / NS) & 1, abort, a.status)) {
@@ -736,7 +747,6 @@ cudaError_t launch_kv_tc(AttnArgs& a, bool fp8, int max_new, cudaStream_t st) {
     const uint32_t tokens = 128 / a.group;
     const int per_block = fp8 ? Cfg<true>::T : Cfg<false>::T;
     a.mr = (int)tokens * a.group * per_block;
-    a.min_run = 2;
     a.max_teams /= per_block;            // as many blocks per SM as keep its tensor memory full
     a.R = team_size(a, a.max_teams, max_new);
     a.max_teams /= a.R;

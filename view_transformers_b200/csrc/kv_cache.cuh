@@ -54,8 +54,7 @@ struct AttnArgs {
     int* desc;                 // [teams] records of kDesc ints: the item a team leaves unfinished
     int max_teams, R;          // R blocks of a team walk the same keys, each for its own query tile
     int mr;                    // rows of a query tile (at most the M of its kernel)
-    int min_run;               // fewest units worth a team of its own
-    Div by_group, by_unit, by_mr, by_R, by_teams, by_run;
+    Div by_group, by_unit, by_mr, by_R, by_teams;
     int32_t* status;
     void set_divisors() {
         by_group = Div(group);
@@ -63,7 +62,6 @@ struct AttnArgs {
         by_mr = Div(mr);
         by_R = Div(R);
         by_teams = Div(max_teams);
-        by_run = Div(min_run);
     }
 };
 constexpr int kDesc = 8;       // valid, first row, tokens, kv head, row group, last team
@@ -153,15 +151,9 @@ struct Start {
     }
     __device__ __forceinline__ void deal(const AttnArgs& a, int units) {
         total = units;
-        const int most = a.by_run.of(units);            // teams that the work is worth
-        teams = max(1, min(a.max_teams, most));
-        run = most >= a.max_teams ? a.by_teams.of(units) : a.min_run;
-        if (teams == 1) run = units;
+        teams = max(1, min(a.max_teams, units));
+        run = units < a.max_teams ? min(units, 1) : a.by_teams.of(units);
         wide = units - run * teams;
-        if (wide > teams) {                             // min_run units each leave more than one a team
-            run = units / teams;
-            wide = units - run * teams;
-        }
     }
 };
 
@@ -392,6 +384,7 @@ struct Rec {
     int row0, pos0, len;   // packed row and position of the chunk's first token, cached tokens
     int h, whole, run;     // key/value head; the segment is the whole item; run of the partial result
     int lo_min, hi_max;    // positions outside the sink that some row sees
+    int lo_max, hi_min;    // [lo_max, hi_min) is seen by every row
 };
 
 // Words of a key tile: a bit per 16 keys whose page exists, and these.
@@ -433,8 +426,8 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
         rec.run = w.has_start ? 1 : 0;
         rec.lo_min = own.lo_min;
         rec.hi_max = own.hi_max;
-        if (!put_record(rec)) return false;
-        if (tiles > 0 && !begin(w, r0)) return false;
+        rec.lo_max = own.lo_max;
+        rec.hi_min = own.hi_min;
         // lane i: box i % boxes of the run's tile jb + i / boxes; the next batch's page ids are on
         // their way while this one's tiles are handed out
         const int bshift = 7 - shift, boxes = 1 << bshift, per = 32 >> bshift;
@@ -445,6 +438,8 @@ __device__ __forceinline__ bool produce(const AttnArgs& a, const Start& start, i
             return j < w.j1 && wanted(k0, box) ? pages[k0 >> a.c.pshift] : -1;
         };
         int ahead = fetch(w.j0), left = tiles;
+        if (!put_record(rec)) return false;
+        if (tiles > 0 && !begin(w, r0)) return false;
         for (int jb = w.j0; left > 0 && jb < w.j1; jb += per) {
             int page = ahead;
             ahead = fetch(jb + per);
