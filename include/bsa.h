@@ -358,7 +358,7 @@ BSA_API bsa_status bsa_attention_noalloc(const bsa_layout* layout, const void* q
  *
  * A cache holds `seqs` independent sequences (streams) of tokens at positions 0, 1, ... in
  * pages of `page_tokens` tokens. Pools are head-major inside a page:
- *   k, v             : device, [pages, kv_heads, page_tokens, 64], bf16 or e4m3
+ *   k, v             : device, [pages, kv_heads, page_tokens, 64], bf16 or e4m3 (finite codes)
  *   k_scale, v_scale : e4m3: device, one byte per row [pages, kv_heads, page_tokens], the
  *                      biased exponent e + 127 of the row's scale 2^e, e within
  *                      [BSA_KV_EXP_MIN, BSA_KV_EXP_MAX] (255: the row is NaN); bf16: unused (NULL)
@@ -437,8 +437,9 @@ BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const in
  *   lse       : device, float32 [heads, rows], or NULL
  *   workspace : device, 16-byte aligned, bsa_kv_workspace_size() bytes; needs no clearing and
  *               keeps nothing between calls; calls that may overlap need one each
- * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product. A call
- * whose work exceeds 2^25 pairs of a query tile (8 to 128 rows) and 128 keys in one sequence is
+ * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product (few rows
+ * over e4m3: to f16, with the value row's scale). A call
+ * whose work exceeds 2^25 pairs of a query tile (8 to 256 rows) and 128 keys in one sequence is
  * refused as BSA_ERR_UNSUPPORTED through status_dev. */
 BSA_API bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max_new, int32_t unit,
                                     int32_t window, int32_t sink, const int32_t* cu_new, const void* q,

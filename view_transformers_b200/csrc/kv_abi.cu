@@ -8,7 +8,7 @@ namespace bsa {
 cudaError_t launch_kv_copy(const kv::CacheArgs& c, bool fp8, bool read, int rows, const int32_t* cu,
                            const int32_t* first, const void* const src[2], void* const dst[2],
                            uint8_t* const scale[2], long long stride, int32_t* status, cudaStream_t st);
-cudaError_t launch_kv_rows(kv::AttnArgs& a, bool fp8, bool eight, cudaStream_t st);
+cudaError_t launch_kv_rows(kv::AttnArgs& a, bool fp8, cudaStream_t st);
 cudaError_t launch_kv_tc(kv::AttnArgs& a, bool fp8, int max_new, cudaStream_t st);
 
 namespace {
@@ -155,21 +155,20 @@ bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + desc_bytes());
     a.status = status_dev;
     a.max_teams = max_blocks();
-    // Query rows of a key/value head, at most, choose the kernel: up to 8 the form for few rows with 8 of
-    // the small instruction's 16 rows, up to 16 that with all 16, else the form for many. Measured
-    // (us; 8 rows, 16 rows, many), 16 heads:
-    //   bf16  1 stream of 78,200 keys, 8 rows:  74.3, 80.7, 67.3; 16 rows:  128, 82.1, 69.1; 17 rows: 183, 138, 68.3
-    //         8 streams of 1,000,      5 rows:  15.6, 19.7, 19.8; 12 rows: 22.0, 20.4, 19.9
-    //         1 stream of 1,000,       5 rows:   9.6, 11.8, 14.2; 12 rows: 10.4, 12.7, 14.3
-    //         6 chunks of 16 rows over up to 95 keys, 4 heads: 7.6 with 16 rows, 17.3 with many
-    //   e4m3  1 stream of 78,200,      8 rows:  48.3, 71.8,  109; 16 rows: 76.4, 75.5,  110; 24 rows: 105, 121, 110
-    //         32 streams of 9,000,     8 rows:   133,  212,  382; 16 rows:  250,  217,  384; 32 rows: 481, 438, 389
-    // In bf16 the form for many is up to 16% faster from 9 rows on, over long caches, but half as fast over
-    // short ones, and the lengths are on the device.
+    // Query rows of a key/value head, at most, choose the kernel: up to 8 (e4m3: 24) the form for few
+    // rows, which reads the cache once per 8 of them, else the form for many. Measured (us; few, many):
+    //   bf16  1 stream of 78,200 keys, 16 heads,  8 rows: 73.5, 65.6; 12 rows:  126, 67.6; 24 rows:  180, 67.5
+    //         8 streams of 1,000 keys,            8 rows: 15.8, 20.7; 12 rows: 22.1, 20.7; 24 rows: 28.3, 20.9
+    //         6 of 95 keys, 4 heads,              8 rows:  6.2, 12.1; 12 rows:  7.3, 12.1; 24 rows:  7.8, 12.1
+    //   e4m3  1 stream of 78,200 keys, 16 heads,  8 rows: 48.8,  111; 24 rows:  105,  112; 32 rows:  134,  110
+    //         32 streams of 9,000 keys,           8 rows:  133,  392; 24 rows:  366,  393; 32 rows:  481,  389
+    //         8 streams of 1,000 keys,            8 rows: 16.4, 28.1; 24 rows: 28.1, 28.3
+    // (The lengths are on the device. 16 rows in one of the few rows' instructions, e4m3: 217 us instead of
+    // 250 for 16 rows on the 32 streams, 25.6 instead of 21.9 on the 8.)
     const bool fp8 = cache->format == BSA_KV_E4M3;
     const long long per_head = (long long)max_new * a.group;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return from_cuda(per_head > 16 ? launch_kv_tc(a, fp8, max_new, st) : launch_kv_rows(a, fp8, per_head <= 8, st));
+    return from_cuda(per_head > (fp8 ? 24 : 8) ? launch_kv_tc(a, fp8, max_new, st) : launch_kv_rows(a, fp8, st));
 }
 
 }  // extern "C"

@@ -7,10 +7,11 @@
 //
 // With few rows the keys and values are read once and nothing else matters: the bound is HBM
 // (128 bytes a row of K or V, 65 in e4m3). So the matrix instruction is the small one (mma.sync),
-// with M rows (8 or 16 of its 16). Measured, one token each: 32 streams of up to 32,768 keys, 32
-// heads over 8, e4m3: 132 us, 4.54 TB/s (0.69 of the copy rate: issue slots bound it, below); 8
-// streams of 16,000 keys, 16 heads, bf16: 109 us, 4.81 TB/s; one token over 7,820 keys: 16.4 us, of
-// which the split of the work, the first loads' latency and the merge are most:
+// with 8 rows of its 16 (the cache is read once per 8 rows). Measured, one token each: 32 streams of
+// up to 32,768 keys, 32 heads over 8, e4m3: 132 us, 4.54 TB/s (0.69 of the copy rate: issue slots
+// bound it, below); 8 streams of 16,000 keys, 16 heads, bf16: 109 us, 4.81 TB/s; one token over
+// 7,820 keys: 16.6 us, of which the split of the work, the first loads' latency and the merge are
+// most.
 //   - a block is eight warps that work alone until an item ends: each takes every eighth group of
 //     16 (bf16) or 32 (e4m3) keys, copies them asynchronously into a ring of its own (pages two
 //     groups ahead, page ids 32 groups ahead, both across items) and keeps its own m, l and O.
@@ -40,12 +41,13 @@ using namespace kv;
 using sm100::ex2_approx;
 
 constexpr int kWarps = 8;
+constexpr int M = 8;                                 // rows of a query tile
 constexpr int kThreads = kWarps * 32;
 constexpr float kScaleLog2 = 0.18033688011112042f;   // log2(e) / sqrt(64)
 constexpr float kRescale = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <bool FP8, int M>
+template <bool FP8>
 struct Cfg {
     static constexpr int kKeys = FP8 ? 32 : 16;                       // keys of a group
     static constexpr int kPer = kUnit / kKeys;                        // groups of a unit
@@ -108,12 +110,11 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-template <bool FP8, int M>
+template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 2)
 kv_rows_kernel(const __grid_constant__ AttnArgs a) {
     using namespace sm100;
-    using C = Cfg<FP8, M>;
-    constexpr int NH = M / 8;               // 8-row halves in use
+    using C = Cfg<FP8>;
     constexpr int GK = C::kKeys;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Start shared_start;
@@ -237,53 +238,43 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
         const int r0 = w.rg * M, nrows = min(M, w.q.n * a.group - r0);
         const Span& sp = w.span;
         // ---------------------------------------------------------------- Q
-        // k-step ks takes the words qf[ks][hh] and qf[ks][NH + hh] of rows 8 hh + g
-        uint32_t qf[4][2 * NH];
-        float rowf[NH];                     // x = score * rowf (e4m3: times the key's scale)
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh) {
-            const int r = hh * 8 + g;
-            uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
-            if (r < nrows) {
-                const int i = a.by_group.of(r0 + r);
-                const uint4* p = reinterpret_cast<const uint4*>(a.q + (long long)(row0 + i) * a.q_stride +
-                                                                ((long long)w.h * a.group + (r0 + r - i * a.group)) * 64);
-                c0 = p[2 * t];
-                c1 = p[2 * t + 1];
-            }
-            uint32_t wds[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            rowf[hh] = kScaleLog2;
-            if (FP8) {
-                // to f16 with the largest element of the row at 2^14 .. 2^15
-                uint32_t top = 0u;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = max(top, max(wds[k] & 0x7fffu, (wds[k] >> 16) & 0x7fffu));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = max((int)(top >> 7) - 14, 1);          // biased exponent of the factor
-                const float inv = pow2_of(254 - e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    wds[k] = pack_half2(__uint_as_float(wds[k] << 16) * inv, __uint_as_float(wds[k] & 0xffff0000u) * inv);
-                rowf[hh] = kScaleLog2 * pow2_of(e);
-            }
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                qf[ks][hh] = wds[2 * ks];
-                qf[ks][NH + hh] = wds[2 * ks + 1];
-            }
+        // k-step ks takes the words qf[ks][0] and qf[ks][1] of row g
+        uint32_t qf[4][2];
+        float rowf = kScaleLog2;            // x = score * rowf (e4m3: times the key's scale)
+        uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
+        if (g < nrows) {
+            const int i = a.by_group.of(r0 + g);
+            const uint4* p = reinterpret_cast<const uint4*>(a.q + (long long)(row0 + i) * a.q_stride +
+                                                            ((long long)w.h * a.group + (r0 + g - i * a.group)) * 64);
+            c0 = p[2 * t];
+            c1 = p[2 * t + 1];
         }
-        float o[8][4];
+        uint32_t wds[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        if (FP8) {
+            // to f16 with the largest element of the row at 2^14 .. 2^15
+            uint32_t top = 0u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, max(wds[k] & 0x7fffu, (wds[k] >> 16) & 0x7fffu));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max((int)(top >> 7) - 14, 1);          // biased exponent of the factor
+            const float inv = pow2_of(254 - e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                wds[k] = pack_half2(__uint_as_float(wds[k] << 16) * inv, __uint_as_float(wds[k] & 0xffff0000u) * inv);
+            rowf = kScaleLog2 * pow2_of(e);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            qf[ks][0] = wds[2 * ks];
+            qf[ks][1] = wds[2 * ks + 1];
+        }
+        float o[8][4];                      // row g: o[j][0] and o[j][1]; the other eight rows stay 0
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
-        float m[NH], l[NH];
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh) {
-            m[hh] = -INFINITY;
-            l[hh] = 0.f;
-        }
+        float m = -INFINITY, l = 0.f;
 
         if constexpr (!FP8) {
 #pragma unroll 1
@@ -311,10 +302,9 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                 const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(x[jj], qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
-                             kw[2 * ks], kw[2 * ks + 1]);
+                    mma_bf16(x[jj], qf[ks][0], 0u, qf[ks][1], 0u, kw[2 * ks], kw[2 * ks + 1]);
 #pragma unroll
-                for (int c = 0; c < 2 * NH; ++c) x[jj][c] *= kScaleLog2;
+                for (int c = 0; c < 2; ++c) x[jj][c] *= kScaleLog2;
             }
             // ------------------------------------------------------------ V, and what is seen
             uint32_t vw[4][4];              // 8 values of the lane's four keys
@@ -327,22 +317,16 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                 vw[i][2] = v.z;
                 vw[i][3] = v.w;
             }
-            uint32_t seen = 0xffu;          // bit (jj * 4 + c): x[jj][c] counts
             if (!all) {
-                seen = 0u;
+                int lo = 0, hi = 0;
+                if (g < nrows) visible(a, len, pos0 + a.by_group.of(r0 + g), lo, hi);
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    const int r = hh * 8 + g;
-                    int lo = 0, hi = 0;
-                    if (r < nrows) visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
+                for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                    for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int key = kb + jj * 8 + 2 * t + c;
-                            if (key < hi && (key >= lo || key < a.sink)) seen |= 1u << (jj * 4 + 2 * hh + c);
-                        }
-                }
+                    for (int c = 0; c < 2; ++c) {
+                        const int key = kb + jj * 8 + 2 * t + c;
+                        if (!(key < hi && (key >= lo || key < a.sink))) x[jj][c] = -INFINITY;
+                    }
                 // P = 0 does not silence a NaN: non-finite values are taken out of V and marked
                 // in the rows that see them (none, past the end)
 #pragma unroll
@@ -365,61 +349,41 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                             }
                         }
                         for (int r = 0; r < nrows; ++r) {
-                            int lo, hi;
-                            visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
-                            if (key < hi && (key >= lo || key < a.sink))
+                            int rlo, rhi;
+                            visible(a, len, pos0 + a.by_group.of(r0 + r), rlo, rhi);
+                            if (key < rhi && (key >= rlo || key < a.sink))
                                 atomicOr(&poison[r][g >> 2], cols << ((g & 3) * 8));
                         }
                     }
                 }
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                    for (int c = 0; c < 2 * NH; ++c)
-                        if (!((seen >> (jj * 4 + c)) & 1u)) x[jj][c] = -INFINITY;
             }
             // ------------------------------------------------------------ softmax
-            float top[NH];
-            bool need = false;
+            const float top = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+            if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                float n = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                n = fmaxf(fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2)), m);
+                const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
+                m = n;
+                l *= f;
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                top[hh] = fmaxf(fmaxf(x[0][2 * hh], x[0][2 * hh + 1]), fmaxf(x[1][2 * hh], x[1][2 * hh + 1]));
-                need |= top[hh] > m[hh] + kRescale;
-            }
-            if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float n = top[hh];
-                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
-                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
-                    n = fmaxf(n, m[hh]);
-                    const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
-                    m[hh] = n;
-                    l[hh] *= f;
-#pragma unroll
-                    for (int j8 = 0; j8 < 8; ++j8) {
-                        o[j8][2 * hh] *= f;
-                        o[j8][2 * hh + 1] *= f;
-                    }
+                for (int j8 = 0; j8 < 8; ++j8) {
+                    o[j8][0] *= f;
+                    o[j8][1] *= f;
                 }
             }
-            uint32_t pf[2][NH];
+            uint32_t pf[2];
+            const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                const float ref = m[hh] == -INFINITY ? 0.f : m[hh];
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const float p0 = ex2_approx(x[jj][2 * hh] - ref), p1 = ex2_approx(x[jj][2 * hh + 1] - ref);
-                    l[hh] += p0 + p1;
-                    pf[jj][hh] = pack_bf16(p0, p1);
-                }
+            for (int jj = 0; jj < 2; ++jj) {
+                const float p0 = ex2_approx(x[jj][0] - ref), p1 = ex2_approx(x[jj][1] - ref);
+                l += p0 + p1;
+                pf[jj] = pack_bf16(p0, p1);
             }
             // ------------------------------------------------------------ O += P V
-            const uint32_t p1a = NH == 2 ? pf[0][NH - 1] : 0u, p1b = NH == 2 ? pf[1][NH - 1] : 0u;
 #pragma unroll
             for (int j8 = 0; j8 < 8; ++j8) {
                 const uint32_t sel = j8 & 1 ? 0x7632u : 0x5410u;
-                mma_bf16(o[j8], pf[0][0], p1a, pf[1][0], p1b, __byte_perm(vw[0][j8 >> 1], vw[1][j8 >> 1], sel),
+                mma_bf16(o[j8], pf[0], 0u, pf[1], 0u, __byte_perm(vw[0][j8 >> 1], vw[1][j8 >> 1], sel),
                          __byte_perm(vw[2][j8 >> 1], vw[3][j8 >> 1], sel));
             }
         }
@@ -442,7 +406,7 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
             const int k1 = 4 + (t ^ 1);                           // key of column 2 t + 1; 2 t: t
             const uint32_t pick = t | k1 << 4;                    // their bytes of two words
             // ------------------------------------------------------------ scores
-            float x[4][2 * NH];
+            float x[4][2];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const uint4 kw = lds16(src + (8 * n + kg) * 64 + t * 16);
@@ -450,10 +414,9 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                 float h[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_f16(h, qf[ks][0], NH == 2 ? qf[ks][NH - 1] : 0u, qf[ks][NH], NH == 2 ? qf[ks][2 * NH - 1] : 0u,
-                            half2_of(kc[ks], false), half2_of(kc[ks], true));
+                    mma_f16(h, qf[ks][0], 0u, qf[ks][1], 0u, half2_of(kc[ks], false), half2_of(kc[ks], true));
 #pragma unroll
-                for (int c = 0; c < 2 * NH; ++c) x[n][c] = h[c];
+                for (int c = 0; c < 2; ++c) x[n][c] = h[c];
             }
             // the rows' scales (NaN for byte 255): a K row's goes into the scores, a V row's into P
             float vs[4][2];
@@ -468,11 +431,8 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                     const float2 v = scales_of(i ? vb4.z : vb4.x, i ? vb4.w : vb4.y, pick);
                     vs[n][0] = v.x;
                     vs[n][1] = v.y;
-#pragma unroll
-                    for (int hh = 0; hh < NH; ++hh) {
-                        x[n][2 * hh] *= ks.x;
-                        x[n][2 * hh + 1] *= ks.y;
-                    }
+                    x[n][0] *= ks.x;
+                    x[n][1] *= ks.y;
                 }
             }
             // ------------------------------------------------------------ V
@@ -484,20 +444,15 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                     vc[half][i] = lds8(src + C::kV + (half * 16 + (i >> 1) * 8 + (i & 1 ? k1 : t)) * 64 + g * 8);
             // ------------------------------------------------------------ what is seen
             if (!all) {
+                int lo = 0, hi = 0;
+                if (g < nrows) visible(a, len, pos0 + a.by_group.of(r0 + g), lo, hi);
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    const int r = hh * 8 + g;
-                    int lo = 0, hi = 0;
-                    if (r < nrows) visible(a, len, pos0 + a.by_group.of(r0 + r), lo, hi);
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int key = kb + 8 * n + (c ? k1 : t);
-                            if (!(key < hi && (key >= lo || key < a.sink) && ((there >> (n >> 1)) & 1)))
-                                x[n][2 * hh + c] = -INFINITY;
-                        }
-                }
+                    for (int c = 0; c < 2; ++c) {
+                        const int key = kb + 8 * n + (c ? k1 : t);
+                        if (!(key < hi && (key >= lo || key < a.sink) && ((there >> (n >> 1)) & 1))) x[n][c] = -INFINITY;
+                    }
                 // stale memory may hold NaN codes (a written row never does: NaN is in its scale)
                 auto clean = [](uint32_t& w) {
                     w &= ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 255u);
@@ -511,60 +466,43 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                     }
             }
             // ------------------------------------------------------------ softmax
-            float top[NH];
-            bool need = false;
+            float top = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                top[hh] = fmaxf(x[0][2 * hh], x[0][2 * hh + 1]);
+            for (int n = 1; n < 4; ++n) top = fmaxf(top, fmaxf(x[n][0], x[n][1]));
+            top *= rowf;
+            if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                float n = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                n = fmaxf(fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2)), m);
+                const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
+                m = n;
+                l *= f;
 #pragma unroll
-                for (int n = 1; n < 4; ++n) top[hh] = fmaxf(top[hh], fmaxf(x[n][2 * hh], x[n][2 * hh + 1]));
-                top[hh] *= rowf[hh];
-                need |= top[hh] > m[hh] + kRescale;
-            }
-            if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float n = top[hh];
-                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
-                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
-                    n = fmaxf(n, m[hh]);
-                    const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
-                    m[hh] = n;
-                    l[hh] *= f;
-#pragma unroll
-                    for (int j8 = 0; j8 < 8; ++j8) {
-                        o[j8][2 * hh] *= f;
-                        o[j8][2 * hh + 1] *= f;
-                    }
+                for (int j8 = 0; j8 < 8; ++j8) {
+                    o[j8][0] *= f;
+                    o[j8][1] *= f;
                 }
             }
-            uint32_t pf[4][NH];               // w of the lane's two keys of each eighth
-            float back[NH];
+            uint32_t pf[4];                   // w of the lane's two keys of each eighth
+            const float ref = m == -INFINITY ? 0.f : m;
+            float p[4][2], top_w = 0.f, sum = 0.f;
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                const float ref = m[hh] == -INFINITY ? 0.f : m[hh];
-                float p[4][2], top_w = 0.f, sum = 0.f;
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int c = 0; c < 2; ++c) {
+                    const float e = ex2_approx(fmaf(x[n][c], rowf, -ref));
+                    sum += e;
+                    // a masked score stays -infinity and its w 0, whatever the scale byte holds
+                    p[n][c] = all || x[n][c] != -INFINITY ? e * vs[n][c] : 0.f;
+                    top_w = fmaxf(top_w, p[n][c]);
+                }
+            l += sum;
+            top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 1));
+            top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 2));
+            // 2^k <= top_w < 2^(k + 1): scaled by 2^(14 - k), undone by back (k kept within -100 .. 100)
+            const int k2 = min(max((int)(__float_as_uint(top_w) >> 23), 27), 227);
+            const float up = pow2_of(268 - k2), back = pow2_of(k2 - 14);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float xv = x[n][2 * hh + c];
-                        const float e = ex2_approx(fmaf(xv, rowf[hh], -ref));
-                        sum += e;
-                        // a masked score stays -infinity and its w 0, whatever the scale byte holds
-                        p[n][c] = all || xv != -INFINITY ? e * vs[n][c] : 0.f;
-                        top_w = fmaxf(top_w, p[n][c]);
-                    }
-                l[hh] += sum;
-                top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 1));
-                top_w = fmaxf(top_w, __shfl_xor_sync(0xffffffffu, top_w, 2));
-                // 2^k <= top_w < 2^(k + 1): scaled by 2^(14 - k), undone by back (k kept within -100 .. 100)
-                const int k = min(max((int)(__float_as_uint(top_w) >> 23), 27), 227);
-                const float up = pow2_of(268 - k);
-                back[hh] = pow2_of(k - 14);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) pf[n][hh] = pack_half2(p[n][0] * up, p[n][1] * up);
-            }
+            for (int n = 0; n < 4; ++n) pf[n] = pack_half2(p[n][0] * up, p[n][1] * up);
             // ------------------------------------------------------------ O += back (w up) V
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -583,11 +521,10 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
                         float h[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
-                            mma_f16(h, pf[2 * half][0], NH == 2 ? pf[2 * half][NH - 1] : 0u, pf[2 * half + 1][0],
-                                    NH == 2 ? pf[2 * half + 1][NH - 1] : 0u, half2_of(ab[half], y), half2_of(cd[half], y));
+                            mma_f16(h, pf[2 * half], 0u, pf[2 * half + 1], 0u, half2_of(ab[half], y), half2_of(cd[half], y));
                         const int j8 = 4 * k + 2 * z + y;
 #pragma unroll
-                        for (int c = 0; c < 2 * NH; ++c) o[j8][c] = fmaf(h[c], back[c >> 1], o[j8][c]);
+                        for (int c = 0; c < 2; ++c) o[j8][c] = fmaf(h[c], back, o[j8][c]);
                     }
                 }
         }
@@ -596,53 +533,41 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
         // -------------------------------------------------------------------- the block's warps
         // warps 4 .. 7 hand theirs to warps 0 .. 3, those the sums to the whole block. Lane (g, t)
         // holds columns 16 t .. 16 t + 15 of row g: o[j][0] is 16 t + j, o[j][1] 8 further
-        auto place = [&](int r, int c, int j8) {
-            return reinterpret_cast<float4*>(mo + ((warp & 3) * M + r) * 64 + 16 * t + 8 * c + j8);
+        auto place = [&](int c, int j8) {
+            return reinterpret_cast<float4*>(mo + ((warp & 3) * M + g) * 64 + 16 * t + 8 * c + j8);
         };
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh) {
-            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
-            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-        }
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
         auto put = [&] {
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                const int r = hh * 8 + g;
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j8 = 0; j8 < 8; j8 += 4)
-                        *place(r, c, j8) = make_float4(o[j8][2 * hh + c], o[j8 + 1][2 * hh + c], o[j8 + 2][2 * hh + c],
-                                                       o[j8 + 3][2 * hh + c]);
-                if (t == 0) {
-                    mml[((warp & 3) * M + r) * 2] = m[hh];
-                    mml[((warp & 3) * M + r) * 2 + 1] = l[hh];
-                }
+                for (int j8 = 0; j8 < 8; j8 += 4)
+                    *place(c, j8) = make_float4(o[j8][c], o[j8 + 1][c], o[j8 + 2][c], o[j8 + 3][c]);
+            if (t == 0) {
+                mml[((warp & 3) * M + g) * 2] = m;
+                mml[((warp & 3) * M + g) * 2 + 1] = l;
             }
         };
         if (warp >= 4) put();
         __syncthreads();
         if (warp < 4) {
+            const float mk = mml[(warp * M + g) * 2], lk = mml[(warp * M + g) * 2 + 1];
+            const float n = fmaxf(m, mk);
+            const float f0 = m == -INFINITY ? 0.f : ex2_approx(m - n);
+            const float f1 = mk == -INFINITY ? 0.f : ex2_approx(mk - n);
+            m = n;
+            l = l * f0 + lk * f1;
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                const int r = hh * 8 + g;
-                const float mk = mml[(warp * M + r) * 2], lk = mml[(warp * M + r) * 2 + 1];
-                const float n = fmaxf(m[hh], mk);
-                const float f0 = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - n);
-                const float f1 = mk == -INFINITY ? 0.f : ex2_approx(mk - n);
-                m[hh] = n;
-                l[hh] = l[hh] * f0 + lk * f1;
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j8 = 0; j8 < 8; j8 += 4) {
-                        const float4 v = *place(r, c, j8);
-                        o[j8][2 * hh + c] = o[j8][2 * hh + c] * f0 + v.x * f1;
-                        o[j8 + 1][2 * hh + c] = o[j8 + 1][2 * hh + c] * f0 + v.y * f1;
-                        o[j8 + 2][2 * hh + c] = o[j8 + 2][2 * hh + c] * f0 + v.z * f1;
-                        o[j8 + 3][2 * hh + c] = o[j8 + 3][2 * hh + c] * f0 + v.w * f1;
-                    }
-            }
+                for (int j8 = 0; j8 < 8; j8 += 4) {
+                    const float4 v = *place(c, j8);
+                    o[j8][c] = o[j8][c] * f0 + v.x * f1;
+                    o[j8 + 1][c] = o[j8 + 1][c] * f0 + v.y * f1;
+                    o[j8 + 2][c] = o[j8 + 2][c] * f0 + v.z * f1;
+                    o[j8 + 3][c] = o[j8 + 3][c] * f0 + v.w * f1;
+                }
             __syncwarp();
             put();
         }
@@ -707,10 +632,11 @@ kv_rows_kernel(const __grid_constant__ AttnArgs a) {
 
 // Joins the partial results of an item that crosses team ends: the team that holds its first
 // unit left it in run 1, the following ones in run 0. L = ln sum e^lse, out = sum e^(lse - L) o,
-// in an order that only the split decides. One block per 16 rows of a (team, member); 16 threads
-// hold a row's columns, and with fewer rows several sets of 16 share a row's pieces.
+// in an order that only the split decides. The blocks of a (team, member) share its rows, at most 16
+// each; 16 threads hold a row's columns, and with fewer rows several sets of 16 share a row's pieces.
+// (Eight pieces' loads at a time instead of four: ragged chunks 100 -> 108 us, for the registers.)
 constexpr int kMergeRows = 16;
-template <int M>
+template <int ROWS>
 __global__ void __launch_bounds__(kMergeRows * 16)
 kv_merge_kernel(const AttnArgs a) {
     __shared__ float4 sacc[kMergeRows][16];
@@ -721,8 +647,14 @@ kv_merge_kernel(const AttnArgs a) {
     const int* d = a.desc + team * kDesc;
     if (d[0] == 0) return;
     const int row0 = d[1], h = d[3], last = d[5];
-    const int r0 = (d[4] * a.R + member) * a.mr, rb = blockIdx.y * kMergeRows;
-    const int nrows = min(min(a.mr, d[2] * a.group - r0) - rb, kMergeRows);
+    const int r0 = (d[4] * a.R + member) * a.mr, rows = min(a.mr, d[2] * a.group - r0);
+    if (rows <= 0) return;                       // a member without rows
+    // rows a block takes: 16, or with many pieces to join as few as the blocks there are allow (16 and 24
+    // rows of 55 and 93 pieces each: 33 -> 22 us a step)
+    const int blocks = gridDim.y;
+    const int per = ROWS <= kMergeRows || last - team < 16 ? kMergeRows : (rows + blocks - 1) / blocks;
+    const int rb = (int)blockIdx.y * per;
+    const int nrows = min(rows - rb, per);
     if (nrows <= 0) return;
     int sets = 1;                                // sets of 16 threads per row: a power of two
     while (nrows * sets * 2 <= kMergeRows) sets *= 2;
@@ -737,9 +669,9 @@ kv_merge_kernel(const AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int kk = min(k + i * sets, last);
-                const float* p = part_at<M>(a, kk, kk == team ? 1 : 0, member) + (rb + r) * 64;
-                v[i] = *reinterpret_cast<const float4*>(p + 4 * c);
-                e[i] = part_at<M>(a, kk, kk == team ? 1 : 0, member)[M * 64 + rb + r] * 1.4426950408889634f;
+                const float* p = part_at<ROWS>(a, kk, kk == team ? 1 : 0, member);
+                v[i] = *reinterpret_cast<const float4*>(p + (rb + r) * 64 + 4 * c);
+                e[i] = part_at<ROWS>(a, kk, kk == team ? 1 : 0, member)[ROWS * 64 + rb + r] * 1.4426950408889634f;
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
@@ -782,10 +714,10 @@ kv_merge_kernel(const AttnArgs a) {
         a.lse[(long long)head * a.rows + row0 + i] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
-template <bool FP8, int M>
+template <bool FP8>
 cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
-    using C = Cfg<FP8, M>;
-    auto kern = kv_rows_kernel<FP8, M>;
+    using C = Cfg<FP8>;
+    auto kern = kv_rows_kernel<FP8>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem, allowed);
     if (e != cudaSuccess) return e;
@@ -794,9 +726,9 @@ cudaError_t launch_rows(AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-template <int M>
+template <int ROWS>
 static cudaError_t launch_merge(const AttnArgs& a, cudaStream_t st) {
-    return launch_early(kv_merge_kernel<M>, dim3(a.max_teams * a.R, (a.mr + kMergeRows - 1) / kMergeRows), kMergeRows * 16, 0,
+    return launch_early(kv_merge_kernel<ROWS>, dim3(a.max_teams * a.R, (a.mr + kMergeRows - 1) / kMergeRows), kMergeRows * 16, 0,
                         st, a);
 }
 
@@ -804,15 +736,12 @@ cudaError_t launch_kv_merge(const AttnArgs& a, bool wide, cudaStream_t st) {
     return wide ? launch_merge<256>(a, st) : launch_merge<128>(a, st);
 }
 
-// 8 rows of a key/value head at a time, or 16
-cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, bool eight, cudaStream_t st) {
+cudaError_t launch_kv_rows(AttnArgs& a, bool fp8, cudaStream_t st) {
     a.R = 1;
-    a.mr = eight ? 8 : 16;
+    a.mr = M;
     a.set_divisors();
-    const cudaError_t e = eight ? (fp8 ? launch_rows<true, 8>(a, st) : launch_rows<false, 8>(a, st))
-                                : (fp8 ? launch_rows<true, 16>(a, st) : launch_rows<false, 16>(a, st));
-    if (e != cudaSuccess) return e;
-    return eight ? launch_merge<8>(a, st) : launch_merge<16>(a, st);
+    const cudaError_t e = fp8 ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
+    return e != cudaSuccess ? e : launch_merge<M>(a, st);
 }
 
 }  // namespace bsa

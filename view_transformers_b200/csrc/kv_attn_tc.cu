@@ -2,10 +2,10 @@
 // key/value head (chunks and frames), on tcgen05. The mathematics is kv_attn.cu's; the bound here
 // is the softmax: a 128 x 128 tile's exponentials (16 a clock and SM) take 1,024 clocks against
 // 650 of matrix instructions, and its other instructions share the four schedulers with them.
-// Measured, 16 heads: a frame of 782 new tokens over 78,200 cached ones in bf16: 371 us, 675
-// TFLOP/s (773 counting the whole tiles, whose last is 11% full). With the exponentials left out
+// Measured, 16 heads: a frame of 782 new tokens over 78,200 cached ones in bf16: 368 us, 681
+// TFLOP/s (780 counting the whole tiles, whose last is 11% full). With the exponentials left out
 // it took 288 us (of 388 then), so the rest of a tile's chain (read S, maximum, write P, products)
-// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 450 us, 566 TFLOP/s.
+// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 447 us, 571 TFLOP/s.
 //
 // A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA warp
 // per query tile (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O
