@@ -438,9 +438,9 @@ BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const in
  *   workspace : device, 16-byte aligned, bsa_kv_workspace_size() bytes; needs no clearing and
  *               keeps nothing between calls; calls that may overlap need one each
  * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product (few rows
- * over e4m3: to f16, with the value row's scale). A call
- * whose work exceeds 2^25 pairs of a query tile (8 to 256 rows) and 128 keys in one sequence is
- * refused as BSA_ERR_UNSUPPORTED through status_dev. */
+ * over e4m3: to f16, with the value row's scale). A call whose work exceeds 2^25 pairs of a query
+ * tile (8 to 256 rows) and 128 keys in one sequence is refused as BSA_ERR_UNSUPPORTED through
+ * status_dev. */
 BSA_API bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max_new, int32_t unit,
                                     int32_t window, int32_t sink, const int32_t* cu_new, const void* q,
                                     int64_t q_stride, void* out, int64_t out_stride, float* lse, void* workspace,

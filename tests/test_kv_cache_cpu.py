@@ -202,3 +202,17 @@ def test_wrapped_tensors_are_checked(lib):
         KVCache.over(k, k, t, n, heads=3)
     with pytest.raises(ValueError):
         _own(fmt="int8")
+
+
+def test_attention_block_checks_its_cache_arguments(lib):
+    from view_transformers_b200.layer import AttentionBlock
+    w = torch.zeros((1, 1), dtype=torch.bfloat16)
+    block = lambda heads=4, **kw: AttentionBlock(1, 20, 5, heads, 64, w, None, w, None, device="cpu", **kw)
+    own = _own(seqs=1, kv_heads=4)
+    assert block(own.heads, cache=own, window=2, anchor=1).sink == 20
+    for kw in (dict(window=1), dict(anchor=1), dict(cache=own, window=-1), dict(cache=own, anchor=-1),
+               dict(cache=own, layer=object())):
+        with pytest.raises(ValueError):
+            block(own.heads, **kw)
+    with pytest.raises(ValueError):
+        block(own.heads * 2, cache=own)

@@ -239,6 +239,8 @@ class AttentionBlock:
                 raise ValueError(f"the cache must hold one sequence of {heads} heads")
         if (window or anchor) and cache is None:
             raise ValueError("window and anchor need a cache")
+        if window < 0 or anchor < 0:
+            raise ValueError("window and anchor must be >= 0")
         self.cache, self.window, self.sink = cache, window, anchor * tokens_per_frame if window else 0
         self.layout = _lib.make_layout(frames, tokens_per_frame, special_per_frame, heads, head_dim,
                                        layer.layout.block if layer is not None else 128, "bf16")
