@@ -28,7 +28,8 @@
  *     Device pointers must be 16-byte aligned.
  *   - Every device call is asynchronous and ordered on `stream` (NULL = legacy stream).
  *   - status_dev: optional device int32 (NULL allowed). Kernels write the first device-
- *     side error (BSA_ERR_TIMEOUT, BSA_ERR_DEVICE_BOUNDS, BSA_ERR_RANGE) there and skip
+ *     side error (BSA_ERR_TIMEOUT, BSA_ERR_DEVICE_BOUNDS, BSA_ERR_RANGE; BSA_ERR_UNSUPPORTED
+ *     where sizes are known on the device only) there and skip
  *     the faulty access instead of faulting; read it with bsa_check_status. Zero it
  *     before use.
  *   - Host-side validation happens before any launch; on error nothing is launched.
@@ -378,8 +379,8 @@ BSA_API bsa_status bsa_attention_noalloc(const bsa_layout* layout, const void* q
  * through status_dev and their accesses skipped. Rows of a page that several sequences share
  * may be read by all of them; two rows appended to one place in one call are a race.
  * Limits (BSA_ERR_UNSUPPORTED): head_dim 64; page_tokens 16, 32, 64, 128 or 256; seqs <=
- * BSA_KV_MAX_SEQS; heads <= BSA_MAX_HEADS; pages * kv_heads * page_tokens and max_pages *
- * page_tokens < 2^31; rows * heads < 2^30; row strides <= 2^38.
+ * BSA_KV_MAX_SEQS; heads <= BSA_MAX_HEADS; pages * kv_heads * page_tokens < 2^31; max_pages *
+ * page_tokens <= 2^30; rows * heads < 2^30; row strides <= 2^38.
  */
 #define BSA_KV_MAX_SEQS 1024
 typedef enum { BSA_KV_BF16 = 0, BSA_KV_E4M3 = 1 } bsa_kv_format;

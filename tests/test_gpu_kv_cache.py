@@ -643,3 +643,23 @@ def test_pools_beyond_32_bit_offsets(fmt):
         out = cache.attend(dev["q"][:k], torch.tensor([0, k], dtype=torch.int32, device="cuda"), k, unit=1, lse=lse)
         check_attention(out, lse, want)
     assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("unit", [0, 1])
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+def test_work_beyond_the_limit_is_refused(max_new, unit):
+    """2^20 new tokens over 2^30 positions (without pages): their products pass 2^32, and the call says so."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    n, P = 1 << 20, 256
+    pool = torch.zeros((1, 1, P, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.full((1, (1 << 30) // P), -1, dtype=torch.int32, device="cuda")
+    cache = KVCache.over(pool, pool.clone(), table, torch.tensor([1 << 30], dtype=torch.int32, device="cuda"), 1)
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    cache.attend(q, torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_new, unit=unit, out=out)
+    assert cache.check_status() == _lib.BSA_ERR_UNSUPPORTED
+    assert bool((out == 7).all())
+    # one token over as many positions is no more than it can do
+    one = cache.attend(q[:1], torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, unit=unit)
+    assert cache.check_status() == 0 and bool((one == 0).all())

@@ -263,7 +263,8 @@ bsa_status bsa_check_status(int32_t* status_dev, bsa_stream_t stream) {
     if (cudaStreamSynchronize(st) != cudaSuccess) return BSA_ERR_CUDA;
     if (v != 0 && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess) return BSA_ERR_CUDA;
     if (v == 0) return BSA_OK;
-    if (v == BSA_ERR_TIMEOUT || v == BSA_ERR_DEVICE_BOUNDS || v == BSA_ERR_RANGE) return (bsa_status)v;
+    if (v == BSA_ERR_UNSUPPORTED || v == BSA_ERR_TIMEOUT || v == BSA_ERR_DEVICE_BOUNDS || v == BSA_ERR_RANGE)
+        return (bsa_status)v;
     return BSA_ERR_CUDA;
 }
 

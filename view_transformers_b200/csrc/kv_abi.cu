@@ -30,8 +30,10 @@ bsa_status check_sizes(const bsa_kv_cache* c) {
     if (c->head_dim != BSA_HEAD_DIM || c->heads > BSA_MAX_HEADS || c->seqs > BSA_KV_MAX_SEQS || c->page_tokens < 16 ||
         c->page_tokens > 256 || (c->page_tokens & (c->page_tokens - 1)) != 0)
         return BSA_ERR_UNSUPPORTED;
-    // pages * kv_heads < 2^38, so the products below stay inside 64 bits
-    if ((int64_t)c->pages * c->kv_heads * c->page_tokens > kMost || (int64_t)c->max_pages * c->page_tokens > kMost)
+    // pages * kv_heads < 2^38, so the products below stay inside 64 bits. Positions stay below 2^30 (kernels
+    // look some thousands ahead of them)
+    if ((int64_t)c->pages * c->kv_heads * c->page_tokens > kMost ||
+        (int64_t)c->max_pages * c->page_tokens > (int64_t)1 << 30)
         return BSA_ERR_UNSUPPORTED;
     return BSA_OK;
 }

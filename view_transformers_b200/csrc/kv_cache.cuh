@@ -172,12 +172,16 @@ __device__ __forceinline__ int lane_sum(int v) {
     return v;
 }
 
-// Units of one key/value head of a sequence with few row groups (long: set instead).
+constexpr int kMostUnits = 1 << 30;
+// Units of one head that are more than any call may have, and whose sum over a warp is an int.
+constexpr int kTooMany = kMostUnits / 32 + 4096;
+
+// Units of one key/value head of a sequence with few row groups (many: far set instead).
 __device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q, bool& far) {
     const int ng = group_count(a, q);
     int u = 0;
     if (a.unit == 0) {
-        u = ng > 0 ? ng * max(1, group_span(a, q, 0).count) : 0;
+        u = ng > 0 ? (int)min((long long)ng * max(1, group_span(a, q, 0).count), (long long)kTooMany) : 0;
     } else if (ng <= 4) {
         for (int g = 0; g < ng; ++g) u += max(1, group_span(a, q, g).count);
     } else {
@@ -189,7 +193,8 @@ __device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q, bool&
 __device__ __forceinline__ int head_units_warp(const AttnArgs& a, const Seq& q, int lane) {
     const int ng = group_count(a, q);
     int u = 0;
-    for (int g = lane; g < ng; g += 32) u += max(1, group_span(a, q, g).count);
+    for (int g = lane; g < ng && u < kTooMany; g += 32) u += max(1, group_span(a, q, g).count);
+    u = min(u, kTooMany);
     return lane_sum(u);
 }
 // the item of unit u0, which lies in the sequence r.q that starts at unit `base` (whole warp)
@@ -215,8 +220,6 @@ __device__ __forceinline__ void find_item(const AttnArgs& a, int base, int per_h
         r.item += all;
     }
 }
-
-constexpr int kMostUnits = 1 << 30;
 
 static __device__ __noinline__ Start plan_many(const AttnArgs& a, int team, int* pre, int* list, Start* st);
 
