@@ -89,16 +89,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// two e4m3 codes (the lower or upper half of w) to f16, exact
-__device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {
-    uint32_t r;
-    if (upper)
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-    else
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
 // the scales whose bytes `pick` takes from two words of scale bytes
 __device__ __forceinline__ float2 scales_of(uint32_t w0, uint32_t w1, uint32_t pick) {
     uint32_t r;

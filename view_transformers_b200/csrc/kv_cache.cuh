@@ -529,6 +529,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// two e4m3 codes (the lower or upper half of w) to f16, exact
+__device__ __forceinline__ uint32_t half2_of(uint32_t w, bool upper) {
+    uint32_t r;
+    if (upper)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
 // 2^(byte - 127), the scale that a scale byte stands for; 255 stands for NaN (a row that held
 // infinite or NaN elements)
 __device__ __forceinline__ float pow2_of(uint32_t byte) { return __uint_as_float(byte << 23); }

@@ -52,13 +52,6 @@ __device__ __forceinline__ void load_cu(const CopyArgs& a, int* cu) {
             if (cu[s] < 0 || cu[s + 1] < cu[s] || cu[s + 1] > a.rows) record_error(a.status, BSA_ERR_DEVICE_BOUNDS);
 }
 
-// e4m3 pair (lower half of w) to f16x2, exact
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
 // First pool row (head 0) of token r, at the stride of heads below; -1: no page, -2: out of range,
 // -3: no sequence holds the token.
 __device__ __forceinline__ long long place_of(const CopyArgs& a, const int* cu, int r, bool read) {
@@ -149,7 +142,7 @@ kv_copy_kernel(const CopyArgs a) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t w = k < 2 ? x[i][0].x : x[i][0].y;
-                        const uint32_t p = e4m3_to_half2(k & 1 ? w >> 16 : w);
+                        const uint32_t p = kv::half2_of(w, k & 1);
                         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
                         o[k] = kv::pack_bf16(v.x * f, v.y * f);   // exact: 4 significant bits times 2^e
                     }
