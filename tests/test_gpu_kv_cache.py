@@ -663,3 +663,50 @@ def test_work_beyond_the_limit_is_refused(max_new, unit):
     # one token over as many positions is no more than it can do
     one = cache.attend(q[:1], torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, unit=unit)
     assert cache.check_status() == 0 and bool((one == 0).all())
+
+
+def _held_up():
+    """Work queued on the current stream that lasts about a tenth of a second."""
+    import torch
+    torch.cuda._sleep(200_000_000)
+
+
+def _filled(n, H=2, pages=24, P=16, fmt="bf16", stream=None):
+    """A cache of its own with n tokens, made and filled on the current stream or on `stream`, and what it then
+    answers for one query: (cache, q, cu_new, out, k, v), computed on one stream with a wait before and after."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    rng = np.random.default_rng(n)
+    k, v, q = (torch.from_numpy(bf16(rng.standard_normal((n, H, D)))).to(torch.bfloat16).cuda() for _ in range(3))
+    cache = KVCache(1, H, H, pages=pages, page_tokens=P, max_pages=pages, fmt=fmt)
+    chunk = cache.extend([n])
+    cache.append(k, v, chunk.cu_new)
+    out = cache.attend(q, chunk.cu_new, n, unit=1)
+    back = cache.read_all(0)
+    torch.cuda.synchronize()
+    assert cache.check_status() == 0
+    return cache, q, chunk.cu_new, out, *back
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_results_on_another_stream_are_not_touched_by_the_current_one(n):
+    """The current stream still has work queued that writes blocks which Python has dropped; the results of calls on
+    another stream, which does not wait for it, take other memory."""
+    import torch
+    cache, q, cu, out, k, v = _filled(n)
+    side = torch.cuda.Stream()
+    calls = (lambda: (cache.attend(q, cu, n, unit=1, stream=side.cuda_stream),),
+             lambda: cache.read(cu, torch.zeros(1, dtype=torch.int32, device="cuda"), rows=n, stream=side.cuda_stream),
+             lambda: cache.read_all(0, stream=side.cuda_stream))
+    for call, want in zip(calls, ((out,), (k, v), (k, v))):
+        dropped = [torch.empty_like(w) for w in want]
+        torch.cuda.synchronize()
+        _held_up()
+        for x in dropped:
+            x.fill_(float("nan"))
+        del dropped, x
+        got = call()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+    assert cache.check_status() == 0

@@ -216,3 +216,39 @@ def test_attention_block_checks_its_cache_arguments(lib):
             block(own.heads, **kw)
     with pytest.raises(ValueError):
         block(own.heads * 2, cache=own)
+
+
+# ------------------------------------------------------------------ streams
+
+def test_results_come_from_the_memory_of_the_stream_that_writes_them(lib, monkeypatch):
+    """A block of the current stream's memory may still be in use by work queued there; a call on another stream
+    does not wait for that work."""
+    import contextlib
+    c = _own()
+    c.extend([20, 3])
+    inside, taken, kept = [], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    empty = torch.empty
+    monkeypatch.setattr(c, "_torch_stream", on)
+    monkeypatch.setattr(c, "_call", lambda *a: None)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (taken.append(inside[-1:]), empty(*a, **k))[1])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: h)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: kept.append(s))
+    q = torch.zeros((23, 4, 64), dtype=torch.bfloat16)
+    cu = torch.tensor([0, 20, 23], dtype=torch.int32)
+    first = torch.zeros(2, dtype=torch.int32)
+    for call, n in ((lambda s: c.attend(q, cu, 20, stream=s), 1), (lambda s: c.read(cu, first, rows=23, stream=s), 2),
+                    (lambda s: c.read_all(0, stream=s), 2)):
+        for stream in (77, None):
+            taken.clear()
+            kept.clear()
+            call(stream)
+            assert taken == [[stream]] * n
+            assert kept == (["current"] * n if stream else [])

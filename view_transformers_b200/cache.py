@@ -128,9 +128,7 @@ class KVCache:
         new tokens of a sequence. lse: optional float32 [heads, rows] for ln sum exp."""
         rows, stride = self._rows("q", q, self.heads)
         if out is None:
-            out = torch.empty((rows, self.heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-            if stream is not None:
-                out.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+            out = self._result(rows, self.heads, stream)
         out_rows, out_stride = self._rows("out", out, self.heads)
         if out_rows != rows:
             raise ValueError("out must have q's rows")
@@ -153,11 +151,7 @@ class KVCache:
         if out is None:
             if rows is None:
                 raise ValueError("read needs rows or out")
-            shape = (rows, self.kv_heads, self.head_dim)
-            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
-            if stream is not None:
-                for x in out:
-                    x.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+            out = tuple(self._result(rows, self.kv_heads, stream) for _ in range(2))
         k, v = out
         n, stride = self._rows("k", k, self.kv_heads)
         if self._rows("v", v, self.kv_heads) != (n, stride):
@@ -243,6 +237,15 @@ class KVCache:
             raise ValueError(f"{name} must be a bf16 tensor [rows, {heads}, {self.head_dim}] on {self.device} whose "
                              "rows are contiguous")
         return shape[0], stride[0] if shape[0] > 1 else heads * self.head_dim
+
+    def _result(self, rows: int, heads: int, stream) -> torch.Tensor:
+        """Memory for a result: that of the stream that writes it (a block of the current stream's memory may
+        still be in use by work queued there), kept for the current stream too, which will read it."""
+        with self._torch_stream(stream):
+            x = torch.empty((rows, heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        if stream is not None:
+            x.record_stream(torch.cuda.current_stream(self.device))
+        return x
 
     def _offsets(self, name: str, x: torch.Tensor, n: int) -> None:
         if x.dtype is not torch.int32 or x.dim() != 1 or len(x) != n or x.device != self.device or not x.is_contiguous():
