@@ -695,8 +695,9 @@ def test_results_on_another_stream_are_not_touched_by_the_current_one(n):
     import torch
     cache, q, cu, out, k, v = _filled(n)
     side = torch.cuda.Stream()
+    first = torch.zeros(1, dtype=torch.int32, device="cuda")
     calls = (lambda: (cache.attend(q, cu, n, unit=1, stream=side.cuda_stream),),
-             lambda: cache.read(cu, torch.zeros(1, dtype=torch.int32, device="cuda"), rows=n, stream=side.cuda_stream),
+             lambda: cache.read(cu, first, rows=n, stream=side.cuda_stream),
              lambda: cache.read_all(0, stream=side.cuda_stream))
     for call, want in zip(calls, ((out,), (k, v), (k, v))):
         dropped = [torch.empty_like(w) for w in want]
