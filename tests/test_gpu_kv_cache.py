@@ -711,3 +711,23 @@ def test_results_on_another_stream_are_not_touched_by_the_current_one(n):
         for g, w in zip(got, want):
             assert torch.equal(g, w)
     assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_a_cache_dropped_while_another_stream_works_on_it(n):
+    """Its memory is given out again only when that stream is done. (What takes it here is as large as the pools; the
+    workspace is of another size class.)"""
+    import torch
+    cache, q, cu, want, k, v = _filled(n)
+    side = torch.cuda.Stream()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        _held_up()
+    cache.attend(q, cu, n, unit=1, out=out, stream=side.cuda_stream)
+    shape = cache.k.shape
+    del cache
+    takers = [torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del takers

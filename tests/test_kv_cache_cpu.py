@@ -252,3 +252,27 @@ def test_results_come_from_the_memory_of_the_stream_that_writes_them(lib, monkey
             call(stream)
             assert taken == [[stream]] * n
             assert kept == (["current"] * n if stream else [])
+
+
+def _on_a_device(c, monkeypatch, current=5):
+    """The cache believes to be on device 0, whose current stream is `current`; streams are their handles."""
+    from view_transformers_b200 import cache
+    c.device, c._index = torch.device("cuda", 0), 0
+    monkeypatch.setattr(cache, "_raw_stream", lambda index: current)
+    monkeypatch.setattr(cache, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: h)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_caches_tensors_are_kept_for_every_stream_that_works_on_them(lib, monkeypatch, fmt):
+    c = _own(fmt=fmt)
+    _on_a_device(c, monkeypatch)
+    own = {t.data_ptr() for t in (c.k, c.v, c.k_scale, c.v_scale, c.page_table, c.kv_len, c.workspace, c.status)
+           if t is not None}
+    kept = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: kept.append((s, x.data_ptr())))
+    used = []
+    for stream in (77, 77, None, 78, None, 77):
+        c._call("call", lambda ref, *a: used.append(a) or 0, stream, "argument")
+    assert used == [("argument", s) for s in (77, 77, 5, 78, 5, 77)]
+    assert sorted(kept) == sorted((s, p) for s in (77, 5, 78) for p in own)

@@ -36,7 +36,11 @@ class Chunk:
 
 class KVCache:
     """One layer's cache. Calls on one KVCache share its workspace and status word: calls that may
-    overlap on the GPU (other streams) need a KVCache each, over the same pools if need be."""
+    overlap on the GPU (other streams) need a KVCache each, over the same pools if need be.
+
+    A call runs on the current stream or on the one whose handle it is given. The cache's own tensors are
+    kept until such work is done; the tensors passed to a call are the caller's to keep, and a stream that
+    was given must live as long as the cache."""
 
     def __init__(self, seqs: int, heads: int, kv_heads: int, pages: int, page_tokens: int, max_pages: int,
                  fmt: str = "bf16", head_dim: int = 64, device: str | torch.device = "cuda"):
@@ -103,6 +107,8 @@ class KVCache:
         self._lib = _lib.load()
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._tensors = tensors + [self.workspace, self.status]
+        self._streams = set()                           # that they are kept for
         self._ref = ctypes.byref(self.c)
         self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
 
@@ -226,6 +232,7 @@ class KVCache:
             raise RuntimeError("the caller keeps this cache's tables")
 
     def _upload(self, stream) -> None:
+        self._on(stream)
         with self._torch_stream(stream):
             self.page_table.copy_(self._table)
             self.kv_len.copy_(torch.tensor(self.lengths, dtype=torch.int32))
@@ -253,8 +260,7 @@ class KVCache:
 
     def _call(self, name: str, fn, stream, *args) -> None:
         """fn(cache, *args, stream) on the cache's device, on its current stream unless one is given."""
-        if stream is None:
-            stream = _raw_stream(self._index)
+        stream = self._on(stream)
         if _current_device() == self._index:
             code = fn(self._ref, *args, stream)
         else:
@@ -262,6 +268,20 @@ class KVCache:
                 code = fn(self._ref, *args, stream)
         if code:
             _lib._check(name, code)
+
+    def _on(self, stream):
+        """The stream's handle: the current one's if none is given. Once for each stream, the cache's tensors are
+        kept for it, so that their memory waits for its work when they are dropped."""
+        if self.device.type != "cuda":
+            return stream
+        if stream is None:
+            stream = _raw_stream(self._index)
+        if stream not in self._streams:
+            other = torch.cuda.ExternalStream(stream, device=self.device)
+            for t in self._tensors:
+                t.record_stream(other)
+            self._streams.add(stream)
+        return stream
 
     def _torch_stream(self, stream):
         if stream is None:
