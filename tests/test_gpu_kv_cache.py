@@ -731,3 +731,54 @@ def test_a_cache_dropped_while_another_stream_works_on_it(n):
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     del takers
+
+
+@pytest.mark.parametrize("own", [True, False], ids=["its_tables", "callers_tables"])
+def test_a_cache_made_behind_queued_work_and_used_on_another_stream(own):
+    """The zeros that it begins with are written before the other stream's first call."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    n, H = 40, 2
+    _, q, cu, want, k, v = _filled(n)
+    side = torch.cuda.Stream()
+    st = side.cuda_stream
+    pool = torch.zeros((3, H, 16, D), dtype=torch.bfloat16, device="cuda")
+    args = (pool, pool.clone(), torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"),
+            torch.tensor([n], dtype=torch.int32, device="cuda"), H)
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    _held_up()
+    if own:
+        cache = KVCache(1, H, H, pages=24, page_tokens=16, max_pages=24)
+        cu = cache.extend([n], stream=st).cu_new
+    else:
+        cache = KVCache.over(*args)
+    cache.append(k, v, cu, stream=st)
+    cache.attend(q, cu, n, unit=1, out=out, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and cache.check_status() == 0
+
+
+def test_a_cache_first_used_or_made_inside_a_capture():
+    import torch
+    from view_transformers_b200.cache import KVCache
+    n, H = 40, 2
+    _, q, cu, want, k, v = _filled(n)
+    pool = torch.zeros((3, H, 16, D), dtype=torch.bfloat16, device="cuda")
+    args = (pool, pool.clone(), torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda"),
+            torch.tensor([n], dtype=torch.int32, device="cuda"), H)
+    out = torch.empty_like(q)
+    caches = [KVCache.over(*args)]
+    for made_inside in (False, True):
+        out.fill_(7.0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if made_inside:
+                caches.append(KVCache.over(*args))
+            caches[-1].append(k, v, cu)
+            caches[-1].attend(q, cu, n, unit=1, out=out)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and caches[-1].check_status() == 0
+        assert torch.equal(caches[-1].attend(q, cu, n, unit=1), want)      # and outside of it
+        del g

@@ -276,3 +276,21 @@ def test_a_caches_tensors_are_kept_for_every_stream_that_works_on_them(lib, monk
         c._call("call", lambda ref, *a: used.append(a) or 0, stream, "argument")
     assert used == [("argument", s) for s in (77, 77, 5, 78, 5, 77)]
     assert sorted(kept) == sorted((s, p) for s in (77, 5, 78) for p in own)
+
+
+def test_a_stream_waits_once_until_the_caches_tensors_are_made(lib, monkeypatch):
+    from view_transformers_b200 import cache
+
+    class Stream(int):
+        def wait_event(self, event):
+            waits.append((int(self), event))
+
+    c = _own()
+    _on_a_device(c, monkeypatch)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: Stream(h))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: None)
+    monkeypatch.setattr(cache, "_capturing", lambda stream: stream == 79)
+    c._made, waits = "made", []
+    for stream in (77, 77, None, 79, 79, 78):
+        c._call("call", lambda ref, *a: 0, stream)
+    assert waits == [(77, "made"), (5, "made"), (78, "made")]

@@ -109,6 +109,10 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._tensors = tensors + [self.workspace, self.status]
         self._streams = set()                           # that they are kept for
+        self._made = None                               # on the stream that made them
+        if self.device.type == "cuda" and not _capturing(current := torch.cuda.current_stream(self.device)):
+            self._made = torch.cuda.Event()
+            self._made.record(current)
         self._ref = ctypes.byref(self.c)
         self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
 
@@ -270,14 +274,17 @@ class KVCache:
             _lib._check(name, code)
 
     def _on(self, stream):
-        """The stream's handle: the current one's if none is given. Once for each stream, the cache's tensors are
-        kept for it, so that their memory waits for its work when they are dropped."""
+        """The stream's handle: the current one's if none is given. Once for each stream, it waits until the
+        cache's tensors are made (a capture needs no wait: it begins with all work done), and they are kept for it,
+        so that their memory waits for its work when they are dropped."""
         if self.device.type != "cuda":
             return stream
         if stream is None:
             stream = _raw_stream(self._index)
         if stream not in self._streams:
             other = torch.cuda.ExternalStream(stream, device=self.device)
+            if self._made is not None and not _capturing(other):
+                other.wait_event(self._made)
             for t in self._tensors:
                 t.record_stream(other)
             self._streams.add(stream)
@@ -292,6 +299,11 @@ class KVCache:
 def _device(device) -> torch.device:
     dev = torch.device(device)
     return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
+
+
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 # current_stream().cuda_stream and current_device() without the objects in between (several
