@@ -782,3 +782,29 @@ def test_a_cache_first_used_or_made_inside_a_capture():
         assert torch.equal(out, want) and caches[-1].check_status() == 0
         assert torch.equal(caches[-1].attend(q, cu, n, unit=1), want)      # and outside of it
         del g
+
+
+def test_a_capture_goes_on_after_refused_changes_of_the_tables():
+    """AttentionBlock(cache=) in a capture too: the refusal comes before the cache counts the frame."""
+    import torch
+    from view_transformers_b200 import layer
+    n, H = 40, 2
+    cache, q, cu, want, *_ = _filled(n)
+    w = torch.zeros((3 * H * D, H * D), dtype=torch.bfloat16, device="cuda")
+    blk = layer.AttentionBlock(1, 20, 5, H, D, w, None, w[:H * D].contiguous(), None, cache=cache)
+    x = torch.zeros((20, H * D), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    free = len(cache._free)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in (lambda: cache.extend([1]), lambda: cache.forget(0, 0, n), lambda: cache.release(0),
+                     lambda: cache.read_all(0), lambda: blk.forward(x)):
+            with pytest.raises(RuntimeError, match="captur"):
+                call()
+        cache.attend(q, cu, n, unit=1, out=out)
+    assert cache.lengths == [n] and len(cache._free) == free
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and cache.check_status() == 0
+    blk.forward(x)
+    assert cache.lengths == [n + 20] and blk.check_status() == 0

@@ -294,3 +294,23 @@ def test_a_stream_waits_once_until_the_caches_tensors_are_made(lib, monkeypatch)
     for stream in (77, 77, None, 79, 79, 78):
         c._call("call", lambda ref, *a: 0, stream)
     assert waits == [(77, "made"), (5, "made"), (78, "made")]
+
+
+def test_what_changes_the_tables_is_refused_in_a_capture_before_any_change(lib, monkeypatch):
+    from view_transformers_b200 import cache
+
+    def fails(*a):
+        raise RuntimeError("operation not permitted when stream is capturing")
+
+    c = _own()
+    c.extend([40, 7])
+    before = list(c.lengths), c._table.clone(), list(c._free)
+    _on_a_device(c, monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: 5)
+    monkeypatch.setattr(cache, "_capturing", lambda stream: True)
+    monkeypatch.setattr(c, "_upload", fails)               # what a copy from host memory does there
+    for call in (lambda: c.extend([1, 1]), lambda: c.extend([1, 1], stream=77), lambda: c.forget(0, 0, 16),
+                 lambda: c.release(0), lambda: c.read_all(0)):
+        with pytest.raises(RuntimeError, match="captur"):
+            call()
+        assert c.lengths == before[0] and torch.equal(c._table, before[1]) and c._free == before[2]

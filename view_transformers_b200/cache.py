@@ -180,8 +180,10 @@ class KVCache:
     # pages and lengths kept by the cache itself ------------------------------------------
     def extend(self, counts, stream: int | None = None) -> Chunk:
         """Makes room for counts[s] new tokens of each sequence: takes pages, updates the device tables (in
-        stream order) and returns the chunk's offsets. Raises before any change if the pages do not suffice."""
-        self._own()
+        stream order) and returns the chunk's offsets. Raises before any change if the pages do not suffice.
+        The tables are copied from host memory, which waits for the stream's earlier work and cannot be
+        captured: capture append and attend, and extend between the replays."""
+        self._own(stream)
         counts = [int(n) for n in counts]
         if len(counts) != self.seqs or min(counts) < 0:
             raise ValueError(f"extend needs {self.seqs} counts >= 0")
@@ -205,7 +207,7 @@ class KVCache:
     def forget(self, seq: int, start: int, stop: int, stream: int | None = None) -> None:
         """Gives back the pages that lie wholly inside positions [start, stop) of a sequence: their tokens no
         longer exist for later calls. The sequence's last page, if not full, stays."""
-        self._own()
+        self._own(stream)
         P = self.page_tokens
         for t in range(-(-max(start, 0) // P), min(stop, self.lengths[seq]) // P):
             if self._table[seq, t] >= 0:
@@ -215,7 +217,7 @@ class KVCache:
 
     def release(self, seq: int, stream: int | None = None) -> None:
         """Empties a sequence."""
-        self._own()
+        self._own(stream)
         self._free += [int(p) for p in self._table[seq] if p >= 0]
         self._table[seq] = -1
         self.lengths[seq] = 0
@@ -223,7 +225,7 @@ class KVCache:
 
     def read_all(self, seq: int, stream: int | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """Every position of a sequence, (k, v) [tokens, kv_heads, 64] bf16."""
-        self._own()
+        self._own(stream)
         n = self.lengths[seq]
         with self._torch_stream(stream):
             cu = torch.tensor([0] * (seq + 1) + [n] * (self.seqs - seq), dtype=torch.int32).to(self.device)
@@ -231,9 +233,13 @@ class KVCache:
         return self.read(cu, first, rows=n, stream=stream)
 
     # helpers ------------------------------------------------------------------------------
-    def _own(self) -> None:
+    def _own(self, stream) -> None:
+        """Refuses, before any change, what needs tables of the cache's own that can be copied from the host now."""
         if self._table is None:
             raise RuntimeError("the caller keeps this cache's tables")
+        if self.device.type == "cuda" and _capturing(torch.cuda.current_stream(self.device) if stream is None
+                                                     else torch.cuda.ExternalStream(stream, device=self.device)):
+            raise RuntimeError("tables copied from the host cannot be part of a capture: call this outside of it")
 
     def _upload(self, stream) -> None:
         self._on(stream)
