@@ -314,3 +314,22 @@ def test_what_changes_the_tables_is_refused_in_a_capture_before_any_change(lib, 
         with pytest.raises(RuntimeError, match="captur"):
             call()
         assert c.lengths == before[0] and torch.equal(c._table, before[1]) and c._free == before[2]
+
+
+def test_sequences_counted_from_the_end(lib, monkeypatch):
+    """read_all(-1) reads the last sequence: its offsets hold all of the result's rows."""
+    c = _own()
+    c.extend([20, 33])
+    got = []
+    monkeypatch.setattr(c, "read", lambda cu, first, rows, stream: got.append((cu.tolist(), rows)))
+    for seq in (-1, 1, 0, -2):
+        c.read_all(seq)
+    assert got == [([0, 0, 33], 33), ([0, 0, 33], 33), ([0, 20, 20], 20), ([0, 20, 20], 20)]
+    for call in (c.read_all, c.release, lambda s: c.forget(s, 0, 20)):
+        for seq in (2, -3):
+            with pytest.raises(IndexError):
+                call(seq)
+    assert c.lengths == [20, 33] and len(c._free) == 1
+    c.forget(-1, 0, 16)
+    c.release(-2)
+    assert c.lengths == [0, 33] and c.page_table[1].tolist()[0] == -1 and len(c._free) == 4

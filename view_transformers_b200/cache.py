@@ -208,6 +208,7 @@ class KVCache:
         """Gives back the pages that lie wholly inside positions [start, stop) of a sequence: their tokens no
         longer exist for later calls. The sequence's last page, if not full, stays."""
         self._own(stream)
+        seq = self._seq(seq)
         P = self.page_tokens
         for t in range(-(-max(start, 0) // P), min(stop, self.lengths[seq]) // P):
             if self._table[seq, t] >= 0:
@@ -218,6 +219,7 @@ class KVCache:
     def release(self, seq: int, stream: int | None = None) -> None:
         """Empties a sequence."""
         self._own(stream)
+        seq = self._seq(seq)
         self._free += [int(p) for p in self._table[seq] if p >= 0]
         self._table[seq] = -1
         self.lengths[seq] = 0
@@ -226,6 +228,7 @@ class KVCache:
     def read_all(self, seq: int, stream: int | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """Every position of a sequence, (k, v) [tokens, kv_heads, 64] bf16."""
         self._own(stream)
+        seq = self._seq(seq)
         n = self.lengths[seq]
         with self._torch_stream(stream):
             cu = torch.tensor([0] * (seq + 1) + [n] * (self.seqs - seq), dtype=torch.int32).to(self.device)
@@ -240,6 +243,12 @@ class KVCache:
         if self.device.type == "cuda" and _capturing(torch.cuda.current_stream(self.device) if stream is None
                                                      else torch.cuda.ExternalStream(stream, device=self.device)):
             raise RuntimeError("tables copied from the host cannot be part of a capture: call this outside of it")
+
+    def _seq(self, seq: int) -> int:
+        """Negative ones count from the end, as in a list."""
+        if not -self.seqs <= seq < self.seqs:
+            raise IndexError(f"sequence {seq} of {self.seqs}")
+        return seq % self.seqs
 
     def _upload(self, stream) -> None:
         self._on(stream)
