@@ -333,3 +333,24 @@ def test_sequences_counted_from_the_end(lib, monkeypatch):
     c.forget(-1, 0, 16)
     c.release(-2)
     assert c.lengths == [0, 33] and c.page_table[1].tolist()[0] == -1 and len(c._free) == 4
+
+
+def test_numbers_beyond_32_bits_are_refused(lib, monkeypatch):
+    """Cut to 32 bits, a window of 2^32 + 1 units would be one of 1."""
+    c = _own()
+    calls = []
+    monkeypatch.setattr(c, "_call", lambda name, fn, stream, *a: calls.append(a[1:5]))
+    q, cu = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for name in ("max_new", "unit", "window", "sink"):
+        for n in (2 ** 31, 2 ** 32 + 1, -2 ** 32 + 1):
+            with pytest.raises(ValueError, match=name):
+                c.attend(q, cu, **{**dict(max_new=3, unit=1, window=1, sink=1), name: n})
+    most = 2 ** 31 - 1
+    c.attend(q, cu, most, unit=most, window=most, sink=most)
+    assert calls == [(most,) * 4]
+    for name in ("seqs", "heads", "kv_heads", "head_dim", "page_tokens", "pages", "max_pages"):
+        good = dict(seqs=2, heads=4, kv_heads=2, head_dim=64, page_tokens=16, pages=6, max_pages=5)[name]
+        with pytest.raises(ValueError, match=name):
+            _own(**{name: 2 ** 32 + good})
+    with pytest.raises(ValueError, match="heads"):
+        KVCache.over(c.k, c.v, c.page_table, c.kv_len, 2 ** 32 + 4, c.k_scale, c.v_scale)

@@ -46,6 +46,8 @@ class KVCache:
                  fmt: str = "bf16", head_dim: int = 64, device: str | torch.device = "cuda"):
         if fmt not in _lib.KV_FORMATS:
             raise ValueError(f"fmt must be one of {tuple(_lib.KV_FORMATS)}")
+        _int32(seqs=seqs, heads=heads, kv_heads=kv_heads, head_dim=head_dim, page_tokens=page_tokens, pages=pages,
+               max_pages=max_pages)
         sizes = _lib.bsa_kv_cache(seqs, heads, kv_heads, head_dim, page_tokens, pages, max_pages,
                                   _lib.KV_FORMATS[fmt])
         _lib.bsa_kv_workspace_size(sizes)              # refuses what the kernels do not take
@@ -91,6 +93,7 @@ class KVCache:
                 tensors.append(t)
         if page_table.dtype != torch.int32 or kv_len.dtype != torch.int32:
             raise ValueError("page_table and kv_len must be int32")
+        _int32(seqs=page_table.shape[0], max_pages=page_table.shape[1], heads=heads)
         if any(t.device != k.device or not t.is_contiguous() for t in tensors):
             raise ValueError("the cache's tensors must be contiguous and on one device")
         self.device, self.heads, self.kv_heads, self.head_dim = k.device, heads, kv_heads, head_dim
@@ -136,6 +139,8 @@ class KVCache:
         the tokens already. unit: tokens per causal unit (tokens per frame: frame-wise; 1: token-wise; 0: all
         see all). window, sink: only the last `window` units and the first `sink` tokens. max_new: the most
         new tokens of a sequence. lse: optional float32 [heads, rows] for ln sum exp."""
+        if max(max_new, unit, window, sink) > _MOST or min(max_new, unit, window, sink) < -_MOST:
+            _int32(max_new=max_new, unit=unit, window=window, sink=sink)
         rows, stride = self._rows("q", q, self.heads)
         if out is None:
             out = self._result(rows, self.heads, stream)
@@ -309,6 +314,16 @@ class KVCache:
         if stream is None:
             return contextlib.nullcontext()
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device))
+
+
+_MOST = 2 ** 31 - 1
+
+
+def _int32(**sizes) -> None:
+    """The ABI's integers have 32 bits; what lies outside would be cut to others without a word."""
+    for name, n in sizes.items():
+        if not -_MOST <= n <= _MOST:
+            raise ValueError(f"{name} = {n} does not fit 32 bits")
 
 
 def _device(device) -> torch.device:
