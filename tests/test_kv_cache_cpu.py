@@ -354,3 +354,18 @@ def test_numbers_beyond_32_bits_are_refused(lib, monkeypatch):
             _own(**{name: 2 ** 32 + good})
     with pytest.raises(ValueError, match="heads"):
         KVCache.over(c.k, c.v, c.page_table, c.kv_len, 2 ** 32 + 4, c.k_scale, c.v_scale)
+
+
+def test_attention_block_refuses_a_cache_that_its_steps_cannot_fill(lib):
+    """When the block is made: a step counts its tokens in the cache before it appends them."""
+    from view_transformers_b200.layer import AttentionBlock
+    w = torch.zeros((1, 1), dtype=torch.bfloat16)
+    own = _own(seqs=1, kv_heads=4)
+    over = KVCache.over(own.k, own.v, own.page_table, own.kv_len, 4, own.k_scale, own.v_scale)
+    block = lambda head_dim=64, device="cpu", **kw: AttentionBlock(1, 20, 5, 4, head_dim, w, None, w, None, device=device, **kw)
+    block(cache=own, window=3, anchor=1)
+    for kw, why in ((dict(cache=own, device="meta"), "on cpu"), (dict(cache=own, head_dim=32), "64 elements"),
+                    (dict(cache=over), "own tables"), (dict(cache=own, window=2 ** 31), "32 bits"),
+                    (dict(cache=own, window=1, anchor=2 ** 31 // 20 + 1), "32 bits")):
+        with pytest.raises(ValueError, match=why):
+            block(**kw)

@@ -119,6 +119,11 @@ class KVCache:
         self._ref = ctypes.byref(self.c)
         self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
 
+    @property
+    def own_tables(self) -> bool:
+        """Whether the cache keeps pages and lengths itself (not KVCache.over)."""
+        return self._table is not None
+
     # steps --------------------------------------------------------------------------
     # A short call is over on the GPU in a few microseconds, so what happens here per call is kept
     # to the checks themselves.
@@ -243,7 +248,7 @@ class KVCache:
     # helpers ------------------------------------------------------------------------------
     def _own(self, stream) -> None:
         """Refuses, before any change, what needs tables of the cache's own that can be copied from the host now."""
-        if self._table is None:
+        if not self.own_tables:
             raise RuntimeError("the caller keeps this cache's tables")
         if self.device.type == "cuda" and _capturing(torch.cuda.current_stream(self.device) if stream is None
                                                      else torch.cuda.ExternalStream(stream, device=self.device)):

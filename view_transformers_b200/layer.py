@@ -237,6 +237,14 @@ class AttentionBlock:
                 raise ValueError("the attention is either a layer or over a cache")
             if (cache.seqs, cache.heads, cache.kv_heads) != (1, heads, heads):
                 raise ValueError(f"the cache must hold one sequence of {heads} heads")
+            if cache.head_dim != head_dim:
+                raise ValueError(f"the cache's heads have {cache.head_dim} elements")
+            if torch.empty(0, device=device).device != cache.device:
+                raise ValueError(f"the cache is on {cache.device}")
+            if not cache.own_tables:
+                raise ValueError("the cache must keep its own tables: each call extends it")
+            if max(window, anchor * tokens_per_frame) >= 2 ** 31:
+                raise ValueError("window and anchor's tokens must fit 32 bits")
         if (window or anchor) and cache is None:
             raise ValueError("window and anchor need a cache")
         if window < 0 or anchor < 0:
