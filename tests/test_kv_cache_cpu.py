@@ -369,3 +369,23 @@ def test_attention_block_refuses_a_cache_that_its_steps_cannot_fill(lib):
                     (dict(cache=own, window=1, anchor=2 ** 31 // 20 + 1), "32 bits")):
         with pytest.raises(ValueError, match=why):
             block(**kw)
+
+
+def test_attention_block_clears_every_status_that_it_checks(lib, monkeypatch):
+    """An error of the cache beside one of the block's own belongs to this check, not to the next."""
+    from view_transformers_b200 import layer
+    w = torch.zeros((1, 1), dtype=torch.bfloat16)
+    own = _own(seqs=1, kv_heads=4)
+    blk = layer.AttentionBlock(1, 20, 5, 4, 64, w, None, w, None, device="cpu", cache=own)
+    status = {blk.status.data_ptr(): 0, "cache": 0}
+
+    def check(key):
+        code, status[key] = status[key], 0
+        return code
+
+    monkeypatch.setattr(_lib, "bsa_check_status", lambda p, stream: check(p))
+    monkeypatch.setattr(own, "check_status", lambda stream: check("cache"))
+    for mine, cache, want in ((0, 0, 0), (5, 0, 5), (0, 6, 6), (5, 6, 5)):
+        status.update({blk.status.data_ptr(): mine, "cache": cache})
+        assert blk.check_status(stream=77) == want
+        assert blk.check_status(stream=77) == 0

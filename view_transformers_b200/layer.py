@@ -287,13 +287,14 @@ class AttentionBlock:
         return self.y
 
     def check_status(self, stream: int | None = None) -> int:
+        """The first error of the projections, the layer and the cache since the last check (0: none)."""
         st = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
-        code = _lib.bsa_check_status(self.status.data_ptr(), st)
+        codes = [_lib.bsa_check_status(self.status.data_ptr(), st)]
         if self.layer is not None:
-            code = code or self.layer.check_status(stream)
+            codes.append(self.layer.check_status(stream))
         if self.cache is not None:
-            code = code or self.cache.check_status(stream)
-        return code
+            codes.append(self.cache.check_status(stream))
+        return next((c for c in codes if c), 0)   # each has been read and cleared
 
 
 def to_device(x, dtype: str, device="cuda") -> torch.Tensor:
