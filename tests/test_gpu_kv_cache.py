@@ -808,3 +808,67 @@ def test_a_capture_goes_on_after_refused_changes_of_the_tables():
     assert torch.equal(out, want) and cache.check_status() == 0
     blk.forward(x)
     assert cache.lengths == [n + 20] and blk.check_status() == 0
+
+
+GROUPS = [Case(f"group{g}_{fmt}", (1, n, 0, 3), (90, n + 150, 7, 300), heads=g * h, kv_heads=h, page=32, fmt=fmt, unit=1)
+          for fmt in ("bf16", "e4m3")
+          for g, h, n in ((5, 2, 60), (7, 2, 40), (12, 3, 25), (16, 1, 20), (33, 1, 9), (100, 1, 5), (128, 1, 5))]
+PAGES = [Case(f"page256_{fmt}", (n,), (1100,), page=256, fmt=fmt, unit=unit, window=w, sink=s, evict=((0, 1),))
+         for fmt in ("bf16", "e4m3") for n, unit, w, s in ((300, 1, 0, 0), (140, 70, 3, 600))]
+
+
+@pytest.mark.parametrize("c", GROUPS + PAGES, ids=str)
+def test_head_groups_and_long_pages_against_the_oracle(c):
+    """Groups that do not divide a query tile, or leave it one token; pages of two key tiles."""
+    x, host = tensors(c)
+    want = attention_oracle(c, host)
+    for mx in (x["max_new"], 1, 2000):
+        cache, out, lse = _attend(c, x, max_new=mx)
+        check_attention(out, lse, want)
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,more,unit,window,sink", [
+    (tuple(500 - 9 * i if i % 8 == 3 else i % 3 for i in range(40)), lambda i: i * 37 % 200, 1, 0, 0),
+    (tuple(500 - 9 * i if i % 8 == 3 else i % 3 for i in range(40)), lambda i: i * 37 % 200, 60, 2, 21),
+    ((190,) * 34, lambda i: i, 1, 0, 0),
+], ids=["mixed", "mixed_window", "alike"])
+def test_long_chunks_of_more_sequences_than_a_warp_has_lanes(fmt, new, more, unit, window, sink):
+    """Chunks of many row groups (of 8, 128 or 256 rows, by max_new) between short and empty ones."""
+    lens = tuple(n + more(i) for i, n in enumerate(new))
+    c = Case("long", new, lens, heads=4, kv_heads=1, page=64, fmt=fmt, unit=unit, window=window, sink=sink)
+    x, host = tensors(c)
+    want = attention_oracle(c, host)
+    for mx in (x["max_new"], 1, 5000):
+        cache, out, lse = _attend(c, x, max_new=mx)
+        check_attention(out, lse, want)
+        assert cache.check_status() == 0
+
+
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+@pytest.mark.parametrize("unit", [0, 1])
+@pytest.mark.parametrize("what", ["one", "sum"])
+def test_work_of_many_sequences_beyond_the_limits_is_refused(what, unit, max_new):
+    """2^25 units (of a query tile and 128 keys) in one sequence, 2^30 in all; positions without pages."""
+    import torch
+    from view_transformers_b200.cache import KVCache
+    S, P, far = 40, 256, 1 << 30
+    # sum: four tiles of 8, 128 rows each in every sequence: 2^25 a sequence, 40 of them
+    n = [1] * S if what == "one" else [4 * (8 if max_new == 1 else 128)] * S
+    if what == "one":
+        n[17] = 1 << 20
+    lens = [far] * S if what == "sum" else [n[i] if i != 17 else far for i in range(S)]
+    pool = torch.zeros((1, 1, P, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.full((S, far // P), -1, dtype=torch.int32, device="cuda")
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache = KVCache.over(pool, pool.clone(), table, length, 1)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+    q = torch.zeros((sum(n), 1, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    cache.attend(q, cu, max_new, unit=unit, out=out)
+    assert cache.check_status() == _lib.BSA_ERR_UNSUPPORTED
+    assert bool((out == 7).all())
+    one = torch.arange(S + 1, dtype=torch.int32, device="cuda")           # one token each over 1,000 positions
+    length.fill_(1000)
+    assert bool((cache.attend(q[:S], one, 1, unit=unit) == 0).all()) and cache.check_status() == 0
