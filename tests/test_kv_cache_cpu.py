@@ -279,8 +279,6 @@ def test_a_caches_tensors_are_kept_for_every_stream_that_works_on_them(lib, monk
 
 
 def test_a_stream_waits_once_until_the_caches_tensors_are_made(lib, monkeypatch):
-    from view_transformers_b200 import cache
-
     class Stream(int):
         def wait_event(self, event):
             waits.append((int(self), event))
@@ -289,7 +287,7 @@ def test_a_stream_waits_once_until_the_caches_tensors_are_made(lib, monkeypatch)
     _on_a_device(c, monkeypatch)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: Stream(h))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: None)
-    monkeypatch.setattr(cache, "_capturing", lambda stream: stream == 79)
+    monkeypatch.setattr(c, "_capturing", lambda stream: stream == 79)
     c._made, waits = "made", []
     for stream in (77, 77, None, 79, 79, 78):
         c._call("call", lambda ref, *a: 0, stream)
@@ -297,8 +295,6 @@ def test_a_stream_waits_once_until_the_caches_tensors_are_made(lib, monkeypatch)
 
 
 def test_what_changes_the_tables_is_refused_in_a_capture_before_any_change(lib, monkeypatch):
-    from view_transformers_b200 import cache
-
     def fails(*a):
         raise RuntimeError("operation not permitted when stream is capturing")
 
@@ -307,7 +303,7 @@ def test_what_changes_the_tables_is_refused_in_a_capture_before_any_change(lib, 
     before = list(c.lengths), c._table.clone(), list(c._free)
     _on_a_device(c, monkeypatch)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: 5)
-    monkeypatch.setattr(cache, "_capturing", lambda stream: True)
+    monkeypatch.setattr(c, "_capturing", lambda stream: True)
     monkeypatch.setattr(c, "_upload", fails)               # what a copy from host memory does there
     for call in (lambda: c.extend([1, 1]), lambda: c.extend([1, 1], stream=77), lambda: c.forget(0, 0, 16),
                  lambda: c.release(0), lambda: c.read_all(0)):

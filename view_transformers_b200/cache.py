@@ -111,11 +111,13 @@ class KVCache:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._tensors = tensors + [self.workspace, self.status]
-        self._streams = set()                           # that they are kept for
-        self._made = None                               # on the stream that made them
-        if self.device.type == "cuda" and not _capturing(current := torch.cuda.current_stream(self.device)):
-            self._made = torch.cuda.Event()
-            self._made.record(current)
+        self._streams = set()                           # that waited for them, and that they are kept for
+        self._made = None                               # on the stream that made them, the first of these
+        if self.device.type == "cuda":
+            self._streams.add(_raw_stream(self._index))
+            if not self._capturing(None):
+                self._made = torch.cuda.Event()
+                self._made.record(torch.cuda.current_stream(self.device))
         self._ref = ctypes.byref(self.c)
         self._ws_ptr, self._status_ptr = self.workspace.data_ptr(), self.status.data_ptr()
 
@@ -144,7 +146,7 @@ class KVCache:
         the tokens already. unit: tokens per causal unit (tokens per frame: frame-wise; 1: token-wise; 0: all
         see all). window, sink: only the last `window` units and the first `sink` tokens. max_new: the most
         new tokens of a sequence. lse: optional float32 [heads, rows] for ln sum exp."""
-        if max(max_new, unit, window, sink) > _MOST or min(max_new, unit, window, sink) < -_MOST:
+        if (max_new | unit | window | sink) >> 31:
             _int32(max_new=max_new, unit=unit, window=window, sink=sink)
         rows, stride = self._rows("q", q, self.heads)
         if out is None:
@@ -209,10 +211,7 @@ class KVCache:
                 self._table[s, t] = self._free.pop()
             self.lengths[s] += counts[s]
             cu.append(cu[-1] + counts[s])
-        self._upload(stream)
-        with self._torch_stream(stream):
-            cu_new = torch.tensor(cu, dtype=torch.int32).to(self.device)
-        return Chunk(cu_new, max(counts), cu[-1])
+        return Chunk(self._upload(stream, cu), max(counts), cu[-1])
 
     def forget(self, seq: int, start: int, stop: int, stream: int | None = None) -> None:
         """Gives back the pages that lie wholly inside positions [start, stop) of a sequence: their tokens no
@@ -250,8 +249,7 @@ class KVCache:
         """Refuses, before any change, what needs tables of the cache's own that can be copied from the host now."""
         if not self.own_tables:
             raise RuntimeError("the caller keeps this cache's tables")
-        if self.device.type == "cuda" and _capturing(torch.cuda.current_stream(self.device) if stream is None
-                                                     else torch.cuda.ExternalStream(stream, device=self.device)):
+        if self.device.type == "cuda" and self._capturing(stream):
             raise RuntimeError("tables copied from the host cannot be part of a capture: call this outside of it")
 
     def _seq(self, seq: int) -> int:
@@ -260,11 +258,16 @@ class KVCache:
             raise IndexError(f"sequence {seq} of {self.seqs}")
         return seq % self.seqs
 
-    def _upload(self, stream) -> None:
-        self._on(stream)
+    def _upload(self, stream, cu=()) -> torch.Tensor:
+        """The tables to the device; offsets too, as a tensor of their own."""
+        if self.device.type == "cuda":
+            handle = _raw_stream(self._index) if stream is None else stream
+            if handle not in self._streams:
+                self._join(handle)
         with self._torch_stream(stream):
             self.page_table.copy_(self._table)
             self.kv_len.copy_(torch.tensor(self.lengths, dtype=torch.int32))
+            return torch.tensor(cu, dtype=torch.int32).to(self.device)
 
     def _rows(self, name: str, x: torch.Tensor, heads: int) -> tuple[int, int]:
         shape, stride = x.shape, x.stride()
@@ -289,7 +292,10 @@ class KVCache:
 
     def _call(self, name: str, fn, stream, *args) -> None:
         """fn(cache, *args, stream) on the cache's device, on its current stream unless one is given."""
-        stream = self._on(stream)
+        if stream is None:
+            stream = _raw_stream(self._index)
+        if stream not in self._streams:
+            self._join(stream)
         if _current_device() == self._index:
             code = fn(self._ref, *args, stream)
         else:
@@ -298,22 +304,25 @@ class KVCache:
         if code:
             _lib._check(name, code)
 
-    def _on(self, stream):
-        """The stream's handle: the current one's if none is given. Once for each stream, it waits until the
-        cache's tensors are made (a capture needs no wait: it begins with all work done), and they are kept for it,
-        so that their memory waits for its work when they are dropped."""
-        if self.device.type != "cuda":
-            return stream
-        if stream is None:
-            stream = _raw_stream(self._index)
-        if stream not in self._streams:
-            other = torch.cuda.ExternalStream(stream, device=self.device)
-            if self._made is not None and not _capturing(other):
-                other.wait_event(self._made)
-            for t in self._tensors:
-                t.record_stream(other)
-            self._streams.add(stream)
-        return stream
+    def _join(self, stream: int) -> None:
+        """Once for each stream: it waits until the cache's tensors are made (a capture needs no wait: it begins
+        with all work done), and they are kept for it, so that their memory waits for its work when they are
+        dropped."""
+        other = torch.cuda.ExternalStream(stream, device=self.device)
+        if self._made is not None and not self._capturing(stream):
+            other.wait_event(self._made)
+        for t in self._tensors:
+            t.record_stream(other)
+        self._streams.add(stream)
+
+    def _capturing(self, stream) -> bool:
+        if stream is None or stream == _raw_stream(self._index):
+            if _current_device() == self._index:
+                return torch.cuda.is_current_stream_capturing()
+            with torch.cuda.device(self.device):
+                return torch.cuda.is_current_stream_capturing()
+        with self._torch_stream(stream):
+            return torch.cuda.is_current_stream_capturing()
 
     def _torch_stream(self, stream):
         if stream is None:
@@ -334,11 +343,6 @@ def _int32(**sizes) -> None:
 def _device(device) -> torch.device:
     dev = torch.device(device)
     return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
-
-
-def _capturing(stream) -> bool:
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
 
 
 # current_stream().cuda_stream and current_device() without the objects in between (several
