@@ -433,15 +433,19 @@ BSA_API bsa_status bsa_kv_read(const bsa_kv_cache* cache, int32_t rows, const in
  * same scores. A token that sees nothing, or only scores of -inf, gets out = 0 and lse = -inf.
  * Keys and values at positions that a token does not see never reach its result, whatever they
  * hold; a NaN or infinite value that it does see makes the elements it enters non-finite.
- *   max_new   : the largest n_s, or an upper bound; only the choice of kernel depends on it
+ *   max_new   : the largest n_s, or an upper bound; only the choice of kernel, and with it the rows
+ *               of a query tile (below), depends on it
  *   q, out    : device, bf16 [rows, heads, 64] with q_stride, out_stride elements between rows
  *   lse       : device, float32 [heads, rows], or NULL
  *   workspace : device, 16-byte aligned, bsa_kv_workspace_size() bytes; needs no clearing and
  *               keeps nothing between calls; calls that may overlap need one each
  * fp32 accumulation and softmax statistics; P is rounded to bf16 for the P.V product (few rows
- * over e4m3: to f16, with the value row's scale). A call whose work exceeds 2^25 pairs of a query
- * tile (8 to 256 rows) and 128 keys in one sequence is refused as BSA_ERR_UNSUPPORTED through
- * status_dev. */
+ * over e4m3: to f16, with the value row's scale). Work is counted in pairs of a
+ * query tile and 128 keys, over all key/value heads. A tile has 8 rows if max_new * heads / kv_heads
+ * <= 8 (e4m3: 24), else up to 128 (e4m3: 256), several neighbouring tiles counting once where they
+ * share their keys; with a max_new below the largest n_s, long chunks are counted in tiles of 8. A call
+ * with more than 2^25 pairs in one sequence or 2^30 in all is refused as BSA_ERR_UNSUPPORTED through
+ * status_dev, and writes nothing. */
 BSA_API bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max_new, int32_t unit,
                                     int32_t window, int32_t sink, const int32_t* cu_new, const void* q,
                                     int64_t q_stride, void* out, int64_t out_stride, float* lse, void* workspace,

@@ -145,7 +145,8 @@ class KVCache:
         """Attention of the new tokens' queries ([rows, heads, 64] bf16) over their sequences, which hold
         the tokens already. unit: tokens per causal unit (tokens per frame: frame-wise; 1: token-wise; 0: all
         see all). window, sink: only the last `window` units and the first `sink` tokens. max_new: the most
-        new tokens of a sequence. lse: optional float32 [heads, rows] for ln sum exp."""
+        new tokens of a sequence, or a bound; it chooses the kernel. lse: optional float32 [heads, rows] for
+        ln sum exp."""
         if (max_new | unit | window | sink) >> 31:
             _int32(max_new=max_new, unit=unit, window=window, sink=sink)
         rows, stride = self._rows("q", q, self.heads)

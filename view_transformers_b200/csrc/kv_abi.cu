@@ -158,7 +158,8 @@ bsa_status bsa_kv_attention(const bsa_kv_cache* cache, int32_t rows, int32_t max
     a.status = status_dev;
     a.max_teams = max_blocks();
     // Query rows of a key/value head, at most, choose the kernel: up to 8 (e4m3: 24) the form for few
-    // rows, which reads the cache once per 8 of them, else the form for many. Measured (us; few, many):
+    // rows, which reads the cache once per 8 of them, else the form for many. Measured (us in
+    // a chain of graph nodes; few, many):
     //   bf16  1 stream of 78,200 keys, 16 heads,  8 rows: 73.5, 65.6; 12 rows:  126, 67.6; 24 rows:  180, 67.5
     //         8 streams of 1,000 keys,            8 rows: 15.8, 20.7; 12 rows: 22.1, 20.7; 24 rows: 28.3, 20.9
     //         6 of 95 keys, 4 heads,              8 rows:  6.2, 12.1; 12 rows:  7.3, 12.1; 24 rows:  7.8, 12.1

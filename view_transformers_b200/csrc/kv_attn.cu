@@ -7,14 +7,17 @@
 //
 // With few rows the keys and values are read once and nothing else matters: the bound is HBM
 // (128 bytes a row of K or V, 65 in e4m3). So the matrix instruction is the small one (mma.sync),
-// with 8 rows of its 16 (the cache is read once per 8 rows). Measured, one token each: 32 streams of
-// up to 32,768 keys, 32 heads over 8, e4m3: 132 us, 4.54 TB/s (0.69 of the copy rate: issue slots
-// bound it, below); 8 streams of 16,000 keys, 16 heads, bf16: 109 us, 4.81 TB/s; one token over
-// 7,820 keys: 16.6 us, of which the split of the work, the first loads' latency and the merge are
-// most.
+// with 8 rows of its 16 (the cache is read once per 8 rows). Measured on a B200, call by call with other
+// inputs every pass, one token each: 32 streams of up to 32,768 keys, 32 heads over 8, e4m3: 149 us,
+// 4.02 TB/s (0.61 of the copy rate; 132 us in a chain of graph nodes over three sets of inputs); 8
+// streams of 16,000 keys, 16 heads, bf16: 113 us, 4.64 TB/s; one token over 7,820 keys: 17.0 us, of
+// which the split of the work, the first loads' latency and the merge are most. Other steps' times in
+// this file are of such chains. No pipe is at its limit in e4m3 (issue 60%, integer 47%, HBM 54% in
+// the chain): the latency of a group's loads and conversions is not hidden by two blocks an SM.
 //   - a block is eight warps that work alone until an item ends: each takes every eighth group of
-//     16 (bf16) or 32 (e4m3) keys, copies them asynchronously into a ring of its own (pages two
-//     groups ahead, page ids 32 groups ahead, both across items) and keeps its own m, l and O.
+//     16 (bf16) or 32 (e4m3) keys, copies them asynchronously into a ring of its own (two groups
+//     ahead, across items) and keeps its own m, l and O. Page ids are fetched 32 groups at a time, a
+//     lane each, when the 32 before are used up or an item begins; that group's copy waits for them.
 //     (One producer warp with TMA for all eight was measured: at 1,400 to 2,000 clocks a tile it
 //     kept e4m3 at 61% of HBM.)
 //   - a dot product does not care about the order of its terms, so the lane that must hold
@@ -24,8 +27,8 @@
 //     swizzled as they are copied (16-byte chunk c of row r at c ^ (r & 7)); e4m3 rows are not, and
 //     the keys are numbered so that the four rows that a lane quad needs lie next to each other.
 // bf16: P is rounded to bf16.
-// e4m3: the integer pipe (two clocks an instruction) is nearest to a bound, so the codes become f16
-// by the one conversion there is and their scales go elsewhere: a K row's into the scores; a V
+// e4m3: the integer pipe (two clocks an instruction) is the busiest, so the codes become f16 by
+// the one conversion there is and their scales go elsewhere: a K row's into the scores; a V
 // row's, 2^e, into P: w_j = p_j 2^(e_j), rounded to f16 relative to the largest w of the group (full
 // precision over 28 binades, whatever the scales), and the group's product is added to O in fp32
 // at its own scale. Q is f16 too, scaled by a power of two per row, exact for elements within

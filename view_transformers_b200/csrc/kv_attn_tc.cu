@@ -2,10 +2,13 @@
 // key/value head (chunks and frames), on tcgen05. The mathematics is kv_attn.cu's; the bound here
 // is the softmax: a 128 x 128 tile's exponentials (16 a clock and SM) take 1,024 clocks against
 // 650 of matrix instructions, and its other instructions share the four schedulers with them.
-// Measured, 16 heads: a frame of 782 new tokens over 78,200 cached ones in bf16: 368 us, 681
-// TFLOP/s (780 counting the whole tiles, whose last is 11% full). With the exponentials left out
-// it took 288 us (of 388 then), so the rest of a tile's chain (read S, maximum, write P, products)
-// is what stands next. A frame of 1,374 tokens over 33 such frames in e4m3: 447 us, 571 TFLOP/s.
+// Measured on a B200, 16 heads, call by call with other inputs every pass: a frame of 782 new tokens
+// over 78,200 cached ones in bf16: 418 us, 599 TFLOP/s (368 us, 681 TFLOP/s in a chain of graph nodes
+// over three sets of inputs; the last of its seven tiles has 14 rows); a frame of 1,374 tokens over 33
+// such frames in e4m3: 448 us, 569 TFLOP/s. Neither is at a pipe's limit (exponentials 43 to 48%, issue
+// 47 to 55%, tensor 27%): a tile's chain (read S, maximum, exponentials, write P, products) is serial
+// in a thread, and two such chains a scheduler do not hide its latency. With the exponentials left
+// out the frame took 288 us in a chain, of 388 then. The steps' times below are of such chains.
 //
 // A block is that of the global layer's attention (attn_tc.cu): a TMA producer warp, an MMA warp
 // per query tile (S = Q K^T into TMEM columns [0,128), O += P V with P (bf16) in [128,192) and O
@@ -24,7 +27,8 @@
 //     tile once for 256 rows, and leave the registers for whole rows of scores (two blocks of one
 //     tile each measured 494 against 458 us, but 85 against 94 us on 15 chunks of 1 to 199 rows,
 //     most with rows for one tile alone). The schedulers fetch all roles' code, so the conversion's
-//     loop is kept short (unrolled four times: 546 us, once 488, when that was tried; twice 450 now);
+//     loop is kept short: the frame of 1,374 tokens took 546 us with it unrolled four times and 488
+//     with it not unrolled; later, beside the present softmax, 455 not unrolled and 450 twice;
 //   - the R blocks of a team walk the same keys for R neighbouring pieces of a chunk, so that a
 //     key/value tile comes from HBM once for all of them; the runs of teams are as in kv_cache.cuh.
 // Every wait is bounded; a timeout is reported through the status word.

@@ -225,7 +225,8 @@ static __device__ __noinline__ Start plan_many(const AttnArgs& a, int team, int*
 
 // The split of the work, for this block's team. Up to 32 sequences: every warp by itself,
 // without shared memory or a barrier. More: the whole block, through pre (seqs + 1 ints), list
-// (seqs + 1 ints) and *st in shared memory. Work beyond 2^30 units is refused.
+// (seqs + 1 ints) and *st in shared memory. Refused: more than 2^25 units in one sequence, over all
+// its key/value heads, so that sums over 32 of them stay inside 2^30; more than 2^30 in all.
 __device__ __forceinline__ Start plan(const AttnArgs& a, int team, int* pre, int* list, Start* st) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int S = a.c.seqs;

@@ -7,9 +7,10 @@
 // thread per token and one turn ahead, then the rows. Eight threads share a row, four one that is
 // quantised (two 16-byte loads and one 16-byte store each; reading back that way, with two stores
 // of 16 bytes in 32, measured slower). A thread works on kRows rows at once: their loads are
-// issued before the first is used. Measured on a B200: 78,200 tokens of 16 heads appended in bf16
-// at 5.86 TB/s (0.90 of the measured copy rate), read back from e4m3 at 4.9 (0.75); 782 tokens
-// quantised in 4.3 us. 16 or 32 tokens a block and 4 or 8 rows a thread are within 10% for large
+// issued before the first is used. Measured on a B200, call by call with other inputs every
+// pass: 78,200 tokens of 16 heads appended in bf16 at 5.76 TB/s (111 us, 0.88 of the measured copy
+// rate), in e4m3 at 5.14 (94 us, 0.78), read back from e4m3 at 4.9 (98 us, 0.75); 782 tokens quantised
+// in 6.7 us (4.3 in a chain of graph nodes). 16 or 32 tokens a block and 4 or 8 rows a thread are within 10% for large
 // calls; these are the best for small ones.
 #include <cuda_fp8.h>
 

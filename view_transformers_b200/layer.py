@@ -227,7 +227,10 @@ class AttentionBlock:
     With `cache` (a cache.KVCache of one sequence) the block serves a stream of frames: each call
     takes the next `frames` frames, appends their keys and values to the cache and lets every
     token attend over its own frame and the cached ones before it -- with window > 0 only the
-    last `window` frames (its own included) and the first `anchor` frames of the stream."""
+    last `window` frames (its own included) and the first `anchor` frames of the stream. Such a window
+    gives no pages back: cache.forget does, for frames that nothing reads any more; positions go on
+    growing, up to the cache's max_pages. Each call extends the cache from the host (KVCache.extend), so
+    it waits for the projection before and cannot be captured."""
 
     def __init__(self, frames: int, tokens_per_frame: int, special_per_frame: int, heads: int, head_dim: int,
                  w_qkv, b_qkv, w_o, b_o, layer: "BlockSparseLayer | None" = None, device="cuda", cache=None,
